@@ -97,7 +97,7 @@ def draw(rng):
         B = _spread(rng, 1, 96)
         return case | {"B": B, "q": q, "kv": _spread(rng, q, max(q, min(131072, room // B)))}
     q = _spread(rng, 9, 4096)
-    B = rng.choice([1, 1, 1, 2, 3, 6]) if q < 2048 else 1
+    B = min(rng.choice([1, 1, 1, 2, 3, 6]), 8192 // q)
     most = max(q, min(65536, 16 * 2048 * 65536 // (B * q * case["heads"])))
     return case | {"B": B, "q": q, "kv": _spread(rng, q, most), "prefix": rng.choice([0, 0, rng.randrange(1, q)])}
 
