@@ -51,6 +51,7 @@ extern "C" {
 #define MOE_ERR_SLOT (-6)     /* a selected expert had slot -1 or >= n_slots    */
 #define MOE_ERR_TIMEOUT (-7)  /* a bounded device-side wait expired             */
 #define MOE_ERR_STATIC (-8)   /* size beyond moe_route_static's fixed scratch    */
+#define MOE_ERR_PAGES (-9)    /* moe_kv_map: no free pages or table entries left  */
 
 #define MOE_SLOT_REMOTE (-2)  /* slot-table entry: the expert lives on another GPU
                                  (expert parallelism): it contributes zero to this
@@ -291,9 +292,161 @@ int moe_profile_read(const uint8_t* buf, size_t bytes, int* L, int* E, int* n_pa
                      int32_t* inverse);
 double moe_profile_hit_rate(const uint16_t* pairs, int n_pairs, int L, int E, int slots, const uint32_t* hist);
 
+/*
+ * ------------------------------------------------------------------------
+ * The attention half of a decoder layer, beside the expert half above: a paged
+ * key-value cache, the step's bookkeeping, the norm and rotation that fill the
+ * cache, and attention for the same two kinds of step, decode windows and
+ * prompt chunks.  The source pages name an 8-bit KV cache, contexts of up to
+ * 262,144 tokens, windows of 1 + 4 tokens and chunks of 8,192 ("Coder
+ * benchmark record" page, test environment); they give no arithmetic.
+ *
+ * The cache: pages of page_size tokens, addressed by a block table per
+ * request; slot s of the cache is token s % page_size of page s / page_size.
+ * Element (page, token, head, d) of either cache sits at page * page_stride +
+ * token * token_stride + head * head_stride + d, in elements, so token-major
+ * and head-major pages, and keys and values in one allocation, all fit.
+ * Requirements: head_dim 64 or 128 (its elements adjacent); n_heads a multiple
+ * of n_kv_heads, at most MOE_ATTN_MAX_HEADS (query head h reads cached head
+ * h / (n_heads / n_kv_heads)); kv_type MOE_KV_BF16 or MOE_KV_E4M3; strides
+ * multiples of 16 bytes, caches 16-byte aligned; n_pages * page_size below
+ * 2^31.  E4M3 elements stand for code * scale with k_scale / v_scale
+ * [n_kv_heads] fp32 (device), NULL = 1; both NULL for MOE_KV_BF16.
+ */
+#define MOE_KV_BF16 0
+#define MOE_KV_E4M3 1
+#define MOE_ATTN_MAX_HEADS 512
+#define MOE_ATTN_MAX_B 4096        /* requests of one step                         */
+#define MOE_KV_MAP_MAX_T 1048576   /* rows of one moe_kv_map / moe_qk_norm_rope call */
+typedef struct moe_kv_desc {
+    void* k_cache;           /* device */
+    void* v_cache;           /* device */
+    const float* k_scale;    /* device or NULL */
+    const float* v_scale;    /* device or NULL */
+    int64_t page_stride, token_stride, head_stride;
+    int32_t n_pages, page_size;
+    int32_t n_heads, n_kv_heads, head_dim, kv_type;
+    int32_t reserved[2];     /* must be 0 */
+} moe_kv_desc;
+
+/*
+ * A step's block tables and slots from the requests' lengths, on the device in
+ * one launch.  Request b holds kv_len[b] cached tokens and brings q_len[b] new
+ * ones; its tokens take rows cu_q[b] .. cu_q[b + 1] - 1 of the step, T rows in
+ * all, of which the last may be padding.
+ *   kv_len, q_len [B] (device); free_pages [n_free] (device): ids of unused
+ *   pages; block_table [B][table_width] (device): row b already holds the
+ *   ceil(kv_len / page_size) pages of its cached tokens and receives the pages
+ *   of its new ones, from free_pages in request order; other entries stay.
+ *   Outputs (device): kv_len_new [B] = kv_len + q_len; cu_q [B + 1]; position
+ *   [T] = kv_len[b] + row - cu_q[b]; slot [T] = the cache slot of that
+ *   position; n_used [1] = how many of free_pages were taken.  Padding rows
+ *   get position 0 and slot -1.
+ * A request whose new tokens do not fit its table row, or whose pages run past
+ * n_free (requests are served in order), gets no page: slots -1, kv_len_new =
+ * kv_len, MOE_ERR_PAGES latched; attention over its new rows is then not
+ * meaningful.  A negative length counts as 0, and rows past T are dropped,
+ * with MOE_ERR_RANGE latched; a token whose page is negative or past the slot
+ * range gets slot -1 with MOE_ERR_SLOT.  All int32.  0 <= B <= MOE_ATTN_MAX_B,
+ * 0 <= T <= MOE_KV_MAP_MAX_T, page_size, table_width >= 1.  No output may
+ * overlap an input or another output (MOE_ERR_ARG): the lengths are not updated
+ * in place.
+ */
+int moe_kv_map(const int32_t* kv_len, const int32_t* q_len, int B, int page_size, const int32_t* free_pages, int n_free,
+               int32_t* block_table, int table_width, int T, int32_t* kv_len_new, int32_t* cu_q, int32_t* position,
+               int32_t* slot, int32_t* n_used, void* stream);
+
+/*
+ * Rotation frequencies f_i, i < rot_dim / 2, and the factor on cosine and sine.
+ *   MOE_ROPE_PLAIN   f_i = base^(-2i / rot_dim)
+ *   MOE_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   MOE_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   MOE_ROPE_PARTS   by parts: with r_i = original_len f_i / 2 pi turns over
+ *                    the original context and g = clamp((r_i - beta_slow) /
+ *                    (beta_fast - beta_slow), 0, 1): f_i g + f_i (1 - g) /
+ *                    factor; rot_scale = 0.1 ln(factor) + 1 (the published
+ *                    "YaRN" method).  rot_scale = 1 for the others.
+ * inv_freq [rot_dim / 2], rot_scale [1] fp32 (host).  factor >= 1, base > 1.
+ * Unused numbers are ignored.  Host only, no CUDA.
+ */
+#define MOE_ROPE_PLAIN 0
+#define MOE_ROPE_LINEAR 1
+#define MOE_ROPE_BASE 2
+#define MOE_ROPE_PARTS 3
+int moe_rope_inv_freq(int kind, int rot_dim, double base, double factor, double original_len, double beta_fast,
+                      double beta_slow, float* inv_freq, float* rot_scale);
+
+/*
+ * Queries and keys of T rows normed per head and turned by their positions,
+ * keys and values written into the cache, in one pass.
+ *   x <- x / sqrt(mean(x^2) + eps) * norm          (q_norm / k_norm [head_dim]
+ *                                                   fp32 (device); NULL: skip)
+ *   (a, b) <- (a cos - b sin, b cos + a sin) * rot_scale at the angle
+ *   position * inv_freq[i]: a, b are elements i and i + rot_dim / 2 of the head,
+ *   or 2i and 2i + 1 when interleaved != 0; elements from rot_dim on stay.
+ * The angle's product is taken in fp64, the rest in fp32, with one rounding to
+ * the output's type (E4M3: x / scale, beyond +-448 at the end of the range).
+ *   q [T][n_heads][head_dim], k and v [T][n_kv_heads][head_dim] bf16 (device),
+ *   rows q_stride, k_stride, v_stride elements apart (one fused projection
+ *   buffer serves), 16-byte aligned, strides multiples of 8; position, slot
+ *   [T] int32; inv_freq [rot_dim / 2] fp32 (device); q_out rows out_stride
+ *   apart, q itself (same stride) for in place; rot_dim a multiple of 16 up to
+ *   head_dim, 0 = no rotation.
+ * A row with a negative slot is padding: nothing of it is read or written.  A
+ * slot past the cache does the same and latches MOE_ERR_SLOT.  Slots of a call
+ * are distinct (of two rows with one slot, parts of either may stay).
+ */
+int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                     const uint16_t* v, int64_t v_stride, int T, const int32_t* position, const int32_t* slot,
+                     const float* q_norm, const float* k_norm, float eps, const float* inv_freq, int rot_dim,
+                     int interleaved, float rot_scale, uint16_t* q_out, int64_t out_stride, void* stream);
+
+/* Bytes of scratch workspace an attention call with these sizes needs (`ws`,
+ * device, 256-byte aligned); the same for every T and B.  0 for sizes no call
+ * takes.  Calls that may overlap on the GPU need a workspace each.  Host only. */
+size_t moe_attn_workspace_bytes(int T, int B, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Attention of a decode window: each request's 1 to max_q <= MOE_DECODE_MAX_T
+ * newest tokens over its cache, those tokens included (write them first).
+ *   Row t = cu_q[b] + i sits at position pos = kv_len[b] - (cu_q[b + 1] -
+ *   cu_q[b]) + i and sees keys j with j <= pos, or j < prefix[b] (a part of the
+ *   prompt whose tokens see one another), and j > pos - window when window > 0.
+ *   s_j = scale * q . k_j; softcap > 0: softcap * tanh(s_j / softcap); slopes:
+ *   s_j - slopes[head] * |pos - j|.
+ *   out = sum_j softmax(s)_j v_j, rounded to bf16; lse = log sum_j exp(s_j).
+ *   A row that sees no key gives out 0 and lse -inf.
+ *   q [T][n_heads][head_dim] bf16 (device, 16-B aligned, rows q_stride elements
+ *   apart, a multiple of 8); cu_q [B + 1], kv_len [B], block_table
+ *   [B][table_width] int32 (device); slopes [n_heads] fp32 or NULL; prefix [B]
+ *   int32 or NULL; out [T][n_heads][head_dim] bf16, not overlapping q; lse [T]
+ *   [n_heads] fp32 or NULL.  Rows from cu_q[B] on are left as they were.
+ * Scores, maximum, sum and output sums are fp32; the softmax numerators are
+ * rounded to 16 bits (bf16, or fp16 for an E4M3 cache) for the product with v.
+ * Values behind kv_len or hidden by the mask are never used, NaN or not.  The
+ * lengths are read on the device only, so a captured call replays with new
+ * ones.  Rows past max_q of a request and lengths past table_width * page_size
+ * are not read; a page id outside the cache reads as zeros and latches
+ * MOE_ERR_SLOT.  Results do not depend on timing.
+ */
+int moe_attn_decode(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, int T, const int32_t* cu_q,
+                    const int32_t* kv_len, int B, const int32_t* block_table, int table_width, int max_q, float scale,
+                    float softcap, int window, const float* slopes, const int32_t* prefix, uint16_t* out, float* lse,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same for a prompt chunk, T <= MOE_PREFILL_MAX_T rows of any number of
+ * requests (requests do not see one another).
+ */
+int moe_attn_prefill(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, int T, const int32_t* cu_q,
+                     const int32_t* kv_len, int B, const int32_t* block_table, int table_width, float scale,
+                     float softcap, int window, const float* slopes, const int32_t* prefix, uint16_t* out, float* lse,
+                     void* ws, size_t ws_bytes, void* stream);
+
 /* Reads and clears the current device's status word after synchronising
- * `stream`: MOE_OK, MOE_ERR_SLOT or MOE_ERR_TIMEOUT (the first latched), or
- * MOE_ERR_RANGE if an internal index was out of range and replaced (a
+ * `stream`: MOE_OK, MOE_ERR_SLOT, MOE_ERR_PAGES or MOE_ERR_TIMEOUT (the first
+ * latched), or MOE_ERR_RANGE if moe_kv_map met a negative length or more
+ * tokens than rows, or if an internal index was out of range and replaced (a
  * library fault; inputs cannot cause it: non-finite logits rank as -inf).
  * No page defines it: it is the boundary's way of reporting what the device
  * detects without trapping. */

@@ -38,7 +38,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_SHAPE, MOE_ERR_RANGE = 0, -1, -2, -3
 MOE_ERR_WS, MOE_ERR_CUDA, MOE_ERR_SLOT, MOE_ERR_TIMEOUT = -4, -5, -6, -7
-MOE_ERR_STATIC = -8
+MOE_ERR_STATIC, MOE_ERR_PAGES = -8, -9
 MOE_DECODE_MAX_T, MOE_PREFILL_MAX_T, MOE_ROUTER_F64_MAX_T = 8, 8192, 128
 MOE_ROUTE_STATIC_MAX_T, MOE_ROUTE_STATIC_BYTES = 8, 128 * 1024
 
@@ -47,16 +47,29 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_forward_decode", "moe_forwar
            "moe_set_stage_events", "moe_launch_count", "moe_timeout_site", "moe_route_static",
            "moe_debug_set", "moe_workspace_offset", "moe_router_gamma", "moe_profile_bytes",
            "moe_profile_write", "moe_profile_read", "moe_profile_hit_rate", "moe_forward_partial",
-           "moe_finish_rows")
+           "moe_finish_rows", "moe_kv_map", "moe_rope_inv_freq", "moe_qk_norm_rope",
+           "moe_attn_workspace_bytes", "moe_attn_decode", "moe_attn_prefill")
 MOE_SLOT_REMOTE = -2
 MOE_DBG_SPIN_LIMIT, MOE_DBG_BARRIER_EXTRA = 1, 2
 MOE_WS_FAST_LOGITS, MOE_WS_PAIR_OUT, MOE_WS_SLOW_COUNT = 1, 2, 3
+MOE_KV_BF16, MOE_KV_E4M3 = 0, 1
+MOE_ATTN_MAX_HEADS, MOE_ATTN_MAX_B, MOE_KV_MAP_MAX_T = 512, 4096, 1048576
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_PARTS = 0, 1, 2, 3
 
 
 class RouteOut(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_void_p), ("topk_w", ctypes.c_void_p),
                 ("expert_offsets", ctypes.c_void_p), ("perm", ctypes.c_void_p),
                 ("n_rechecked", ctypes.c_void_p)]
+
+
+class KvDesc(ctypes.Structure):
+    """moe_kv_desc of include/moe.h (made by moe_kv_desc below)."""
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("kv_type", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
 
 
 class MoeError(RuntimeError):
@@ -119,6 +132,19 @@ def lib() -> ctypes.CDLL:
         L.moe_profile_read.argtypes = [P, sz, P, P, P, P, P]
         L.moe_profile_hit_rate.restype = ctypes.c_double
         L.moe_profile_hit_rate.argtypes = [P, i32, i32, i32, i32, P]
+        i64, f32, f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+        L.moe_kv_map.restype = i32
+        L.moe_kv_map.argtypes = [P, P, i32, i32, P, i32, P, i32, i32, P, P, P, P, P, P]
+        L.moe_rope_inv_freq.restype = i32
+        L.moe_rope_inv_freq.argtypes = [i32, i32, f64, f64, f64, f64, f64, P, P]
+        L.moe_qk_norm_rope.restype = i32
+        L.moe_qk_norm_rope.argtypes = [P, P, i64, P, i64, P, i64, i32, P, P, P, P, f32, P, i32, i32, f32, P, i64, P]
+        L.moe_attn_workspace_bytes.restype = sz
+        L.moe_attn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        L.moe_attn_decode.restype = i32
+        L.moe_attn_decode.argtypes = [P, P, i64, i32, P, P, i32, P, i32, i32, f32, f32, i32, P, P, P, P, P, sz, P]
+        L.moe_attn_prefill.restype = i32
+        L.moe_attn_prefill.argtypes = [P, P, i64, i32, P, P, i32, P, i32, f32, f32, i32, P, P, P, P, P, sz, P]
         _lib = L
     return _lib
 
@@ -335,3 +361,164 @@ def moe_profile_hit_rate(pairs, L: int, E: int, slots: int, hist) -> float:
     if v < 0:
         raise MoeError(MOE_ERR_ARG, "moe_profile_hit_rate")
     return v
+
+
+# ---------------------------------------------------------------- the attention half of a layer
+
+def _refuse(where, what):
+    raise MoeError(MOE_ERR_ARG, f"{where}: {what}")
+
+
+def _need(ok, where, what):
+    if not ok:
+        _refuse(where, what)
+
+
+def _flat(t, n, dtype, where, what, dev):
+    """Device pointer of n adjacent elements of this type (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
+        _refuse(where, f"{what} is a contiguous {dtype} tensor of at least {n} elements on the current device")
+    return t.data_ptr()
+
+
+def _rows16(t, n, d, where, what, dev):
+    """(pointer, elements from row to row) of a bf16 [T, n, d] tensor whose rows are whole."""
+    import torch
+    st = t.stride()
+    if (t.dim() != 3 or t.shape[1] != n or t.shape[2] != d or st[2] != 1 or (n > 1 and st[1] != d)
+            or t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or t.get_device() != dev):
+        _refuse(where, f"{what} is a bf16 [T, {n}, {d}] tensor with adjacent heads on the current device")
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else max(st[0], n * d)
+
+
+def moe_kv_desc(k_cache, v_cache, n_heads: int, k_scale=None, v_scale=None) -> KvDesc:
+    """Descriptor of a paged cache from its two tensors, both [pages, page size,
+    kv heads, head dim] in any order of strides (a head-major cache is passed
+    transposed); bfloat16 (or int16), or float8_e4m3fn (or uint8) with optional
+    fp32 [kv heads] scales.  It holds the tensors it points to."""
+    import torch
+    where = "moe_kv_desc"
+    wide = (torch.bfloat16, torch.int16, torch.uint16)
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
+          and k_cache.device == v_cache.device and k_cache.is_cuda, where, "two equal 4-d device caches")
+    _need(k_cache.dtype in wide or k_cache.dtype in (torch.float8_e4m3fn, torch.uint8), where, "bf16 or e4m3 caches")
+    pages, size, heads, dim = k_cache.shape
+    strides = []
+    for i in range(4):  # a dimension of one element may have any stride: 0 serves
+        sk, sv = k_cache.stride(i), v_cache.stride(i)
+        _need(sk == sv or k_cache.shape[i] == 1, where, "caches of equal strides")
+        strides.append(sk if k_cache.shape[i] > 1 else 0)
+    _need(strides[3] == 1, where, "adjacent elements of a head")
+    d = KvDesc(k_cache.data_ptr(), v_cache.data_ptr(), None, None, strides[0], strides[1], strides[2], pages, size,
+               n_heads, heads, dim, MOE_KV_BF16 if k_cache.dtype in wide else MOE_KV_E4M3)
+    dev = k_cache.get_device()
+    d.k_scale = _flat(k_scale, heads, torch.float32, where, "k_scale", dev)
+    d.v_scale = _flat(v_scale, heads, torch.float32, where, "v_scale", dev)
+    d.device_index = dev
+    d.held = (k_cache, v_cache, k_scale, v_scale)
+    return d
+
+
+def _on_device(kv, where):
+    import torch
+    dev = torch.cuda.current_device()
+    if kv is not None and getattr(kv, "device_index", dev) != dev:
+        _refuse(where, "the cache is on another device than the current one")
+    return dev
+
+
+def moe_kv_map(kv_len, q_len, page_size, free_pages, block_table, kv_len_new, cu_q, position, slot, n_used,
+               stream=None, raise_on_error=True) -> int:
+    """Block tables, offsets, positions and cache slots of a step's new tokens
+    (all int32 CUDA tensors; position and slot have one entry per row)."""
+    import torch
+    where, i32 = "moe_kv_map", torch.int32
+    dev = _on_device(None, where)
+    B, T = kv_len.numel(), position.numel()
+    _need(block_table.dim() == 2 and block_table.shape[0] == B, where, "block_table is [B, width]")
+    width = block_table.shape[1]
+    rc = lib().moe_kv_map(
+        _flat(kv_len, B, i32, where, "kv_len", dev), _flat(q_len, B, i32, where, "q_len", dev), B, page_size,
+        _flat(free_pages, 0, i32, where, "free_pages", dev), 0 if free_pages is None else free_pages.numel(),
+        _flat(block_table, B * width, i32, where, "block_table", dev), width, T,
+        _flat(kv_len_new, B, i32, where, "kv_len_new", dev), _flat(cu_q, B + 1, i32, where, "cu_q", dev),
+        _flat(position, T, i32, where, "position", dev), _flat(slot, T, i32, where, "slot", dev),
+        _flat(n_used, 1, i32, where, "n_used", dev), _stream(stream))
+    return _check(rc, where, raise_on_error)
+
+
+def moe_qk_norm_rope(kv: KvDesc, q, k, v, position, slot, q_out, inv_freq=None, q_norm=None, k_norm=None, eps=1e-6,
+                     rot_scale=1.0, interleaved=False, stream=None, raise_on_error=True) -> int:
+    """Per-head norm and rotation of q and k [T, heads, dim] bf16, q to q_out
+    (q itself for in place), k and v into the cache at slot [T].  inv_freq fp32
+    [rot_dim / 2] or None (no rotation); q_norm, k_norm fp32 [dim] or None."""
+    import torch
+    where, f32, i32 = "moe_qk_norm_rope", torch.float32, torch.int32
+    dev = _on_device(kv, where)
+    T, D = q.shape[0], kv.head_dim
+    _need(k.shape[0] == T and v.shape[0] == T and q_out.shape[0] == T, where, "q, k, v and q_out have T rows")
+    qp, qs = _rows16(q, kv.n_heads, D, where, "q", dev)
+    kp, ks = _rows16(k, kv.n_kv_heads, D, where, "k", dev)
+    vp, vs = _rows16(v, kv.n_kv_heads, D, where, "v", dev)
+    op, os_ = _rows16(q_out, kv.n_heads, D, where, "q_out", dev)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    rc = lib().moe_qk_norm_rope(
+        ctypes.byref(kv), qp, qs, kp, ks, vp, vs, T, _flat(position, T, i32, where, "position", dev),
+        _flat(slot, T, i32, where, "slot", dev), _flat(q_norm, D, f32, where, "q_norm", dev),
+        _flat(k_norm, D, f32, where, "k_norm", dev), eps, _flat(inv_freq, rot // 2, f32, where, "inv_freq", dev), rot,
+        int(bool(interleaved)), rot_scale, op, os_, _stream(stream))
+    return _check(rc, where, raise_on_error)
+
+
+def moe_attn_workspace_bytes(T: int, B: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().moe_attn_workspace_bytes(T, B, n_heads, n_kv_heads, head_dim))
+
+
+def _attn(fn, where, max_q, kv, q, cu_q, kv_len, block_table, out, ws, scale, softcap, window, slopes, prefix, lse,
+          stream, raise_on_error):
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    dev = _on_device(kv, where)
+    T, D, B = q.shape[0], kv.head_dim, kv_len.numel()
+    qp, qs = _rows16(q, kv.n_heads, D, where, "q", dev)
+    _need(block_table.dim() == 2 and block_table.shape[0] == B, where, "block_table is [B, width]")
+    width = block_table.shape[1]
+    _need(out.shape[0] == T and out.is_contiguous(), where, "out is contiguous with T rows")
+    op, _ = _rows16(out, kv.n_heads, D, where, "out", dev)
+    _need(ws.get_device() == dev and ws.is_contiguous(), where, "ws is a contiguous tensor on the current device")
+    rc = fn(ctypes.byref(kv), qp, qs, T, _flat(cu_q, B + 1, i32, where, "cu_q", dev),
+            _flat(kv_len, B, i32, where, "kv_len", dev), B,
+            _flat(block_table, B * width, i32, where, "block_table", dev), width, *max_q, scale, softcap, window,
+            _flat(slopes, kv.n_heads, f32, where, "slopes", dev), _flat(prefix, B, i32, where, "prefix", dev), op,
+            _flat(lse, T * kv.n_heads, f32, where, "lse", dev), ws.data_ptr(), ws.numel() * ws.element_size(),
+            _stream(stream))
+    return _check(rc, where, raise_on_error)
+
+
+def moe_attn_decode(kv: KvDesc, q, cu_q, kv_len, block_table, out, max_q, ws, scale, softcap=0.0, window=0, slopes=None,
+                    prefix=None, lse=None, stream=None, raise_on_error=True) -> int:
+    """Attention of windows of 1 to max_q <= 8 new tokens a request over the
+    paged cache (include/moe.h); q, out [T, heads, dim] bf16, lse [T, heads]."""
+    return _attn(lib().moe_attn_decode, "moe_attn_decode", (max_q,), kv, q, cu_q, kv_len, block_table, out, ws, scale,
+                 softcap, window, slopes, prefix, lse, stream, raise_on_error)
+
+
+def moe_attn_prefill(kv: KvDesc, q, cu_q, kv_len, block_table, out, ws, scale, softcap=0.0, window=0, slopes=None,
+                     prefix=None, lse=None, stream=None, raise_on_error=True) -> int:
+    """Attention of a prompt chunk of T <= 8192 rows over the paged cache."""
+    return _attn(lib().moe_attn_prefill, "moe_attn_prefill", (), kv, q, cu_q, kv_len, block_table, out, ws, scale,
+                 softcap, window, slopes, prefix, lse, stream, raise_on_error)
+
+
+def moe_rope_inv_freq(rot_dim: int, base: float, kind: int = MOE_ROPE_PLAIN, factor: float = 1.0,
+                      original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(numpy fp32 [rot_dim / 2] frequencies, factor on cosine and sine); include/moe.h gives the kinds."""
+    import numpy as np
+    f = np.zeros(max(rot_dim // 2, 1), np.float32)
+    s = ctypes.c_float(0.0)
+    rc = lib().moe_rope_inv_freq(kind, rot_dim, base, factor, original_len, beta_fast, beta_slow,
+                                 f.ctypes.data_as(ctypes.c_void_p), ctypes.byref(s))
+    _check(rc, "moe_rope_inv_freq", True)
+    return f, s.value

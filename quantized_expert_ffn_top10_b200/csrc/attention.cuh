@@ -1,0 +1,766 @@
+// Attention over the paged key-value cache.  For a query row (token i of
+// request b, head) at position pos = kv_len - n_new + i, over its visible keys
+// j in [lo, hi), hi = max(pos + 1, min(prefix, kv_len)), lo = max(0, pos - W + 1):
+//   s_j = scale q . k_j, capped: cap tanh(s_j / cap), less slope |pos - j|
+//   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
+// One pass over the keys with a running maximum and sum, all of it fp32.
+//
+// The rows of a request that share a cached head (its new tokens x the group of
+// G = heads / kv_heads query heads, row = token * G + g) are cut into row tiles;
+// a row tile and a cached head is an item, and an item is a run of key tiles.
+// All key tiles of the call, in order, are dealt out evenly: each CTA of a grid
+// that fills the GPU takes the same number of consecutive tiles, whatever the
+// lengths, which only the device knows.  An item that falls into one CTA is
+// written by it; one that is cut leaves fp32 partial sums, which a second kernel
+// joins in order (so results do not depend on timing).
+#pragma once
+
+#include "common.cuh"
+
+#define ATT_MAX_CTAS 304        // 2 x 152: workspace is sized for this many
+#define ATT_PART_ROWS 64        // rows of partial sums per SM and slot (32 x 2 CTAs, or 64)
+#define ATT_JOIN_WARPS 8
+
+struct AttnArgs {
+    const uint16_t* q;
+    int64_t q_stride;  // elements from token to token
+    const uint8_t *k, *v;
+    const float *k_scale, *v_scale;
+    int64_t page_b, token_b, head_b;  // bytes
+    int n_pages, page_size;
+    const int32_t *cu, *kv_len, *table;
+    int width, T, B, Hk, G, max_q, window;
+    float scale, softcap;
+    const float* slopes;
+    const int32_t* prefix;
+    uint16_t* out;
+    float* lse;
+    float* part;   // [2 * CTAs][rows][D]
+    float2* ml;    // [2 * CTAs][rows]: exponent reference (base 2) and sum
+    int4* hdr;     // [CTAs]: {parts, first token, row of the request, cached head} of the item cut at this CTA's end
+    int32_t* hdr_rows;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 8 x 8 transpose of 16-bit elements across the warp
+__device__ __forceinline__ uint32_t mat_t(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8); A and B fp16 or bf16
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// two e4m3 (low 16 bits) -> two fp16, exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
+    uint32_t y;
+    asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// A request's rows and lengths, with every device-side number clamped to what the call's arguments allow.
+struct AttSeq {
+    int t0, n, kv, pre;
+};
+__device__ __forceinline__ AttSeq att_seq(const AttnArgs& a, int b) {
+    AttSeq s;
+    s.t0 = min(max(a.cu[b], 0), a.T);
+    s.n = min(min(max(a.cu[b + 1], s.t0), a.T) - s.t0, a.max_q);
+    s.kv = min(max(a.kv_len[b], 0), (int)min((int64_t)a.width * a.page_size, (int64_t)0x7fffffff));
+    s.pre = a.prefix ? min(max(a.prefix[b], 0), s.kv) : 0;
+    return s;
+}
+// visible keys [lo, hi) of token i of the request
+__device__ __forceinline__ void att_range(const AttnArgs& a, const AttSeq& s, int i, int& lo, int& hi) {
+    const int pos = s.kv - s.n + i;
+    hi = max(max(pos + 1, s.pre), 0);
+    lo = a.window ? max(0, pos - a.window + 1) : 0;
+}
+
+// An item's position in the deal: row tile rt of request b for cached head h, key tile `tile` of n.
+struct AttCur {
+    int b, rt, h, tile, n, lo, hi;
+    AttSeq s;
+};
+
+template <int ROWS, int TK>
+__device__ __forceinline__ int att_tiles(const AttnArgs& a, const AttSeq& s, int rt, int& lo, int& hi) {
+    const int i0 = rt * ROWS / a.G, i1 = min(s.n - 1, (rt * ROWS + ROWS - 1) / a.G);
+    int l1, h0;
+    att_range(a, s, i0, lo, h0);
+    att_range(a, s, i1, l1, hi);
+    return hi > lo ? (hi - lo + TK - 1) / TK : 1;  // a row tile without a key still has its rows to write
+}
+
+template <int ROWS, int TK>
+__device__ __forceinline__ void att_enter(const AttnArgs& a, AttCur& c) {
+    c.n = att_tiles<ROWS, TK>(a, c.s, c.rt, c.lo, c.hi);
+}
+
+// Next key tile in the deal's order: tiles of an item, cached heads of a row tile, row tiles, requests.
+template <int ROWS, int TK>
+__device__ __forceinline__ void att_next(const AttnArgs& a, AttCur& c) {
+    if (++c.tile < c.n) return;
+    c.tile = 0;
+    if (++c.h < a.Hk) return;
+    c.h = 0;
+    if ((++c.rt) * ROWS >= c.s.n * a.G) {
+        c.rt = 0;
+        do {
+            if (++c.b >= a.B) return;
+            c.s = att_seq(a, c.b);
+        } while (c.s.n == 0);
+    }
+    att_enter<ROWS, TK>(a, c);
+}
+
+// The deal: total tiles, tiles per CTA, and where this CTA starts.  Every CTA
+// computes it for itself, with two block scans: row tiles per request (kept in
+// `base`, B + 1 ints of shared memory), then key tiles per row tile.
+template <int ROWS, int TK, int NTH>
+__device__ void att_deal(const AttnArgs& a, int* base, int64_t* red, AttCur& c, int64_t& w0, int64_t& per, int64_t& total) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_b, s_rt;
+    __shared__ int64_t s_before;
+    auto scan = [&](int64_t v, int64_t& all) {  // exclusive over the block
+        int64_t inc = v;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t t = __shfl_up_sync(~0u, inc, d);
+            if (lane >= d) inc += t;
+        }
+        __syncthreads();
+        if (lane == 31) red[warp] = inc;
+        __syncthreads();
+        int64_t ex = inc - v;
+        all = 0;
+        for (int w = 0; w < NTH / 32; ++w) {
+            if (w < warp) ex += red[w];
+            all += red[w];
+        }
+        return ex;
+    };
+    const int ipt = (a.B + NTH - 1) / NTH, b0 = min(a.B, tid * ipt), b1 = min(a.B, b0 + ipt);
+    int64_t mine = 0, entries;
+    for (int b = b0; b < b1; ++b) mine += ((int64_t)att_seq(a, b).n * a.G + ROWS - 1) / ROWS;
+    int64_t ex = scan(mine, entries);
+    for (int b = b0; b < b1; ++b) {
+        base[b] = (int)ex;
+        ex += ((int64_t)att_seq(a, b).n * a.G + ROWS - 1) / ROWS;
+    }
+    if (tid == 0) base[a.B] = (int)entries;
+    __syncthreads();
+    const int ept = (int)((entries + NTH - 1) / NTH), e0 = min((int)entries, tid * ept), e1 = min((int)entries, e0 + ept);
+    auto find = [&](int e) {  // the last request that starts at or before entry e
+        int lo = 0, hi = a.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (base[mid] <= e) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    int64_t tiles = 0;
+    int b = e0 < e1 ? find(e0) : 0;
+    int first_b = b;
+    AttSeq s = att_seq(a, b);
+    int lo, hi;
+    for (int e = e0; e < e1; ++e) {
+        if (e >= base[b + 1]) {
+            do ++b; while (base[b + 1] <= e);
+            s = att_seq(a, b);
+        }
+        tiles += att_tiles<ROWS, TK>(a, s, e - base[b], lo, hi);
+    }
+    int64_t all;
+    const int64_t before = scan(tiles, all);
+    total = all * a.Hk;
+    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
+    w0 = per * blockIdx.x;
+    if (w0 < total) {
+        const int64_t at = w0 / a.Hk;  // the entry that holds tile `at` of one head holds w0
+        if (at >= before && at < before + tiles) {
+            int64_t p = before;
+            b = first_b;
+            s = att_seq(a, b);
+            for (int e = e0; e < e1; ++e) {
+                if (e >= base[b + 1]) {
+                    do ++b; while (base[b + 1] <= e);
+                    s = att_seq(a, b);
+                }
+                const int n = att_tiles<ROWS, TK>(a, s, e - base[b], lo, hi);
+                if (at < p + n) {
+                    s_b = b;
+                    s_rt = e - base[b];
+                    s_before = p;
+                    break;
+                }
+                p += n;
+            }
+        }
+        __syncthreads();
+        c.b = s_b;
+        c.rt = s_rt;
+        c.s = att_seq(a, c.b);
+        att_enter<ROWS, TK>(a, c);
+        const int64_t rem = w0 - s_before * a.Hk;
+        c.h = (int)(rem / c.n);
+        c.tile = (int)(rem % c.n);
+    }
+}
+
+template <int D, bool F8, int NTW, int RW, int KW>
+struct AttCfg {
+    static constexpr int ES = F8 ? 1 : 2, CH = D * ES / 16;     // 16-byte chunks of a cached row
+    static constexpr int NTH = 32 * RW * KW, ROWS = 8 * NTW * RW;
+    static constexpr int PER_SM = NTH > 128 ? 1 : 2;
+    static constexpr int TK = 32768 / (2 * D * ES) > 128 ? 128 : 32768 / (2 * D * ES);
+    static constexpr int STAGE = 2 * TK * D * ES;
+    static constexpr int ST = (PER_SM == 2 ? 98304 : 163840) / STAGE;  // 3 to 10 stages
+    static constexpr int KPW = TK / KW;                          // keys of a warp in a tile
+    static constexpr int CK = KPW > 32 ? 32 : KPW;               // and in one softmax step
+    static constexpr int AROW = D + 4;                           // merge areas, one per row group, padded against bank conflicts
+    static constexpr int AREA_B = 8 * NTW * AROW * 4;
+    static constexpr int OFF_AREA = ST * STAGE, OFF_ML = OFF_AREA + RW * AREA_B;
+    static constexpr int OFF_ROW = OFF_ML + RW * 8 * NTW * 8, SMEM = OFF_ROW + ST * TK * 8;
+    static_assert(TK <= NTH || TK == 128, "one thread looks up one key");
+    static_assert(PER_SM * (SMEM + 128 + 1024) <= 233472, "the CTAs of an SM share its 228 KB");
+    static_assert((4097 + 64) * 4 <= OFF_AREA, "the deal's scan borrows the stages");
+};
+
+// One warp's share: RW row groups of 8 NTW rows x KW key groups.  The products
+// are taken transposed, S^T = K Q^T and O^T += V^T P^T, so that the rows are the
+// 8-wide side of mma.m16n8k16: a single query head wastes no more than 7 of 8
+// columns, and K (as stored) and V (through ldmatrix.trans) are the A operands.
+// e4m3 rows are widened to fp16, exactly; queries are then scaled by a power of
+// two per row so that no bf16 value leaves fp16's range, and the softmax
+// numerators by 2^10, so that those down to 2^-34 of the largest still count.
+template <int D, bool F8, int NTW, int RW, int KW>
+__global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8, NTW, RW, KW>::PER_SM)
+    k_attn_rows(const AttnArgs a) {
+    using C = AttCfg<D, F8, NTW, RW, KW>;
+    constexpr int TK = C::TK, CH = C::CH, ES = C::ES, NTH = C::NTH, ROWS = C::ROWS, ST = C::ST, CK = C::CK;
+    constexpr int SUB = CK / 16, MT = D / 16;
+    constexpr float LOG2E = 1.4426950408889634f;
+    constexpr float LIFT = F8 ? 10.f : 0.f;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int64_t* offs = reinterpret_cast<int64_t*>(smem + C::OFF_ROW);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rw = warp % RW, kw = warp / RW, qd = lane & 3, g8 = lane >> 2;
+    const uint32_t sb = smem_u32(smem);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    AttCur pre;
+    int64_t w0, per, total;
+    att_deal<ROWS, TK, NTH>(a, reinterpret_cast<int*>(smem), reinterpret_cast<int64_t*>(smem + C::OFF_AREA), pre, w0, per,
+                            total);
+    const int my = (int)max((int64_t)0, min(per, total - w0));
+    if (my == 0) {
+        if (tid == 0) a.hdr[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    __syncthreads();  // the scan's shared memory is free
+    AttCur cur = pre;
+
+    // ---- loads: the page of tile p + 1 is fetched while tile p's row offsets are handed over
+    int pg = 0, pg_off = 0, pg_head = 0;
+    bool pg_live = false;
+    int pre_n = 0;  // tiles whose page has been asked for
+    auto fetch = [&] {
+        if (pre_n < my && tid < TK) {
+            const int key = pre.lo + pre.tile * TK + tid;
+            pg_live = key < pre.hi;
+            pg_head = pre.h;
+            if (pg_live) {
+                const int col = key / a.page_size;
+                pg_off = key - col * a.page_size;
+                pg = __ldg(a.table + (int64_t)pre.b * a.width + col);
+            }
+        }
+        if (pre_n < my) {
+            ++pre_n;
+            if (pre_n < my) att_next<ROWS, TK>(a, pre);
+        }
+    };
+    auto hand_over = [&](int p) {
+        if (p < my && tid < TK) {
+            int64_t o = -1;
+            if (pg_live) {
+                if (pg >= 0 && pg < a.n_pages) o = pg * a.page_b + pg_off * a.token_b + pg_head * a.head_b;
+                else moe_set_status(MOE_ERR_SLOT);  // its keys read as zeros
+            }
+            offs[(p % ST) * TK + tid] = o;
+        }
+    };
+    auto issue = [&](int p) {
+        if (p < my) {
+            const uint32_t st = sb + (p % ST) * C::STAGE;
+            const int c = tid % CH;
+#pragma unroll
+            for (int r0 = 0; r0 < TK; r0 += NTH / CH) {
+                const int r = r0 + tid / CH;
+                const int64_t o = offs[(p % ST) * TK + r];
+                const int sw = CH >= 8 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                const uint32_t dst = st + r * (CH * 16) + sw * 16;
+                const int64_t src = (o < 0 ? 0 : o) + c * 16;
+                cp_async16(dst, a.k + src, o >= 0);
+                cp_async16(dst + TK * CH * 16, a.v + src, o >= 0);
+            }
+        }
+        cp_async_commit();
+    };
+    fetch();
+    for (int p = 0; p < ST - 1; ++p) {
+        if (p < my) {
+            hand_over(p);
+            fetch();
+            __syncthreads();
+        }
+        issue(p);
+    }
+    hand_over(ST - 1);
+    fetch();
+
+    // ---- state of an item
+    uint32_t qf[NTW][MT][2];
+    float acc[NTW][MT][4], m[NTW][2], l[NTW][2], rs[NTW][2], slope[NTW][2];
+    int rlo[NTW][2], rhi[NTW][2], rpos[NTW][2];
+    int all_lo = 0, all_hi = 0;  // keys that every row of the tile sees
+    float vs = 1.f;
+    bool started = false;
+
+    for (int it = 0; it < my; ++it) {
+        cp_async_wait<ST - 2>();
+        __syncthreads();
+        issue(it + ST - 1);
+        hand_over(it + ST);
+        fetch();
+
+        if (!started) {
+            started = true;
+            const float ks = (F8 && a.k_scale) ? __ldg(a.k_scale + cur.h) : 1.f;
+            vs = (F8 && a.v_scale) ? __ldg(a.v_scale + cur.h) : 1.f;
+            const int rows = min(ROWS, cur.s.n * a.G - cur.rt * ROWS);
+            int t_lo, t_hi;
+            att_range(a, cur.s, cur.rt * ROWS / a.G, t_lo, all_hi);
+            att_range(a, cur.s, (cur.rt * ROWS + rows - 1) / a.G, all_lo, t_hi);
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt) {
+                const int r = (rw * NTW + nt) * 8 + g8, rr = cur.rt * ROWS + r;
+                const int i = rr / a.G, head = cur.h * a.G + rr % a.G;
+                const uint16_t* qp = a.q + (int64_t)(cur.s.t0 + i) * a.q_stride + head * D;
+                const bool live = r < rows;
+#pragma unroll
+                for (int k = 0; k < MT; ++k) {
+                    if constexpr (F8) {
+                        uint2 w = live ? *reinterpret_cast<const uint2*>(qp + k * 16 + qd * 4) : make_uint2(0, 0);
+                        qf[nt][k][0] = w.x;
+                        qf[nt][k][1] = w.y;
+                    } else {
+                        qf[nt][k][0] = live ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + qd * 2) : 0u;
+                        qf[nt][k][1] = live ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + qd * 2 + 8) : 0u;
+                    }
+                }
+                float unit = 1.f;
+                if constexpr (F8) {  // bring the row's largest element to [2^14, 2^15)
+                    float top = 0.f;
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[nt][k][j] << 16)),
+                                                   fabsf(__uint_as_float(qf[nt][k][j] & 0xffff0000u))));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    const int be = (int)(__float_as_uint(top) >> 23);
+                    const int e = be == 255 ? 0 : max(be - 127 - 14, -100);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+                    unit = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            qf[nt][k][j] = pack_f16x2(__uint_as_float(qf[nt][k][j] << 16) * down,
+                                                      __uint_as_float(qf[nt][k][j] & 0xffff0000u) * down);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // the rows of this lane's accumulators
+                    const int r2 = (rw * NTW + nt) * 8 + qd * 2 + j, rr2 = cur.rt * ROWS + r2;
+                    rs[nt][j] = a.scale * ks * __shfl_sync(~0u, unit, (qd * 2 + j) * 4) * (a.softcap > 0.f ? 1.f : LOG2E);
+                    rlo[nt][j] = rhi[nt][j] = 0;
+                    rpos[nt][j] = cur.s.kv - cur.s.n + rr2 / a.G;
+                    slope[nt][j] = 0.f;
+                    if (r2 < rows) {
+                        att_range(a, cur.s, rr2 / a.G, rlo[nt][j], rhi[nt][j]);
+                        if (a.slopes) slope[nt][j] = __ldg(a.slopes + cur.h * a.G + rr2 % a.G) * LOG2E;
+                    }
+                    m[nt][j] = -INFINITY;
+                    l[nt][j] = 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < MT; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[nt][k][j] = 0.f;
+            }
+        }
+
+        // ---- one key tile
+        const uint32_t st = sb + (it % ST) * C::STAGE, stv = st + TK * CH * 16;
+        const int k0 = cur.lo + cur.tile * TK;
+        const bool masked = k0 < all_lo || k0 + TK > all_hi;
+        auto chunk_addr = [&](uint32_t base, int row, int c) {
+            const int sw = CH >= 8 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+            return base + row * (CH * 16) + sw * 16;
+        };
+#pragma unroll 1
+        for (int kc = 0; kc < C::KPW; kc += CK) {
+            const int kr = kw * C::KPW + kc;  // first key row of this step in the tile
+            float s[NTW][SUB][4];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[nt][u][j] = 0.f;
+                const int row = kr + u * 16 + (lane & 15);
+                if constexpr (F8) {
+#pragma unroll
+                    for (int k2 = 0; k2 < MT / 2; ++k2) {
+                        uint32_t r[4];
+                        ldsm4(r, chunk_addr(st, row, k2 * 2 + (lane >> 4)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t fa[4] = {e4m3x2_to_f16x2(r[2 * h]), e4m3x2_to_f16x2(r[2 * h + 1]),
+                                                    e4m3x2_to_f16x2(r[2 * h] >> 16), e4m3x2_to_f16x2(r[2 * h + 1] >> 16)};
+#pragma unroll
+                            for (int nt = 0; nt < NTW; ++nt)
+                                mma16816<true>(s[nt][u], fa, qf[nt][2 * k2 + h][0], qf[nt][2 * k2 + h][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k) {
+                        uint32_t fa[4];
+                        ldsm4(fa, chunk_addr(st, row, k * 2 + (lane >> 4)));
+#pragma unroll
+                        for (int nt = 0; nt < NTW; ++nt) mma16816<false>(s[nt][u], fa, qf[nt][k][0], qf[nt][k][1]);
+                    }
+                }
+            }
+            // scores in base 2; this lane holds keys kr + 16 u + g8 (+ 8) of rows 2 qd and 2 qd + 1
+            uint32_t pb[NTW][SUB][2];
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt) {
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
+                        float x = s[nt][u][e] * rs[nt][j];
+                        if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
+                            const float y = ex2(x * (2.f * LOG2E) / a.softcap);
+                            x = (a.softcap * LOG2E) * (1.f - __fdividef(2.f, 1.f + y));
+                        }
+                        if (a.slopes) x -= slope[nt][j] * fabsf((float)(rpos[nt][j] - key));
+                        if (masked) x = (key >= rlo[nt][j] && key < rhi[nt][j]) ? x : -INFINITY;
+                        s[nt][u][e] = x;
+                        top[j] = fmaxf(top[j], x);
+                    }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(~0u, top[j], d));
+                }
+                const bool grew = top[0] > m[nt][0] || top[1] > m[nt][1];
+                if (__any_sync(~0u, grew)) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float mn = fmaxf(m[nt][j], top[j]);
+                        const float f = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mn);
+                        m[nt][j] = mn;
+                        l[nt][j] *= f;
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            acc[nt][k][j] *= f;
+                            acc[nt][k][2 + j] *= f;
+                        }
+                    }
+                }
+                const float ref[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0] - LIFT, m[nt][1] == -INFINITY ? 0.f : m[nt][1] - LIFT};
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(s[nt][u][e] - ref[e & 1]);
+                        l[nt][e & 1] += p[e];
+                    }
+                    // the numerators are rounded once more, to the cache's 16-bit type, for the product with V;
+                    // the sum above takes them unrounded
+                    pb[nt][u][0] = mat_t(F8 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
+                    pb[nt][u][1] = mat_t(F8 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
+                }
+            }
+            // O^T += V^T P^T.  In a tile with masked places a zero numerator may meet an infinite or
+            // NaN value that its row must not see: those values are taken out of the product here
+            // and added below to the rows that do see them.
+            bool odd = false;
+            auto clean = [&](uint32_t x) {
+                constexpr uint32_t EXP = F8 ? 0x7c00u : 0x7f80u;
+                uint32_t keep = 0xffffffffu;
+                if ((x & EXP) == EXP) keep &= 0xffff0000u;
+                if (((x >> 16) & EXP) == EXP) keep &= 0x0000ffffu;
+                odd |= keep != 0xffffffffu;
+                return x & keep;
+            };
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+                if constexpr (F8) {
+#pragma unroll
+                    for (int k2 = 0; k2 < MT / 2; ++k2) {
+                        uint32_t r[4];
+                        ldsm4t(r, chunk_addr(stv, kr + u * 16 + (lane & 15), k2 * 2 + (lane >> 4)));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x0 = e4m3x2_to_f16x2(r[2 * h]), x1 = e4m3x2_to_f16x2(r[2 * h] >> 16);
+                            const uint32_t y0 = e4m3x2_to_f16x2(r[2 * h + 1]), y1 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
+                            uint32_t fa[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                                              __byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
+                            if (masked) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NTW; ++nt)
+                                mma16816<true>(acc[nt][2 * k2 + h], fa, pb[nt][u][0], pb[nt][u][1]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k) {
+                        uint32_t fa[4];
+                        ldsm4t(fa, chunk_addr(stv, kr + u * 16 + (lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
+                        if (masked) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NTW; ++nt) mma16816<false>(acc[nt][k], fa, pb[nt][u][0], pb[nt][u][1]);
+                    }
+                }
+            }
+            if (masked && __any_sync(~0u, odd)) {
+#pragma unroll
+                for (int k = 0; k < MT; ++k)
+#pragma unroll
+                    for (int d2 = 0; d2 < 2; ++d2) {
+                        const int d = F8 ? k * 16 + g8 * 2 + d2 : k * 16 + g8 + d2 * 8;
+#pragma unroll 1
+                        for (int r = kr; r < kr + CK; ++r) {
+                            const uint32_t at = chunk_addr(stv, r, d * ES / 16) - sb + (d * ES) % 16;
+                            float x;
+                            if constexpr (F8) {
+                                const uint32_t hx = e4m3x2_to_f16x2(smem[at]);
+                                x = half_bits_to_f32((uint16_t)hx);
+                            } else {
+                                x = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(smem + at));
+                            }
+                            if (fabsf(x) < INFINITY) continue;
+#pragma unroll
+                            for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (k0 + r >= rlo[nt][j] && k0 + r < rhi[nt][j]) acc[nt][k][2 * d2 + j] += x;
+                        }
+                    }
+            }
+        }
+
+        // ---- the item ends here: join the key groups, write the rows or their partial sums
+        const bool last = cur.tile == cur.n - 1;
+        if (last || it == my - 1) {
+            started = false;
+#pragma unroll
+            for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], d);
+                }
+            float* const ar = reinterpret_cast<float*>(smem + C::OFF_AREA + rw * C::AREA_B);
+            float2* const mls = reinterpret_cast<float2*>(smem + C::OFF_ML) + rw * 8 * NTW;
+            auto dim = [&](int k, int d2) { return F8 ? k * 16 + g8 * 2 + d2 : k * 16 + g8 + d2 * 8; };
+            auto put = [&] {
+#pragma unroll
+                for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = nt * 8 + qd * 2 + j;
+                        if (g8 == 0) mls[r] = make_float2(m[nt][j], l[nt][j]);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            ar[r * C::AROW + dim(t, 0)] = acc[nt][t][j];
+                            ar[r * C::AROW + dim(t, 1)] = acc[nt][t][2 + j];
+                        }
+                    }
+            };
+#pragma unroll 1
+            for (int from = 1; from < KW; ++from) {  // the first key group takes in the others, one at a time
+                if (kw == from) put();
+                __syncthreads();
+                if (kw == 0) {
+#pragma unroll
+                    for (int nt = 0; nt < NTW; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = nt * 8 + qd * 2 + j;
+                            const float2 o = mls[r];
+                            const float mn = fmaxf(m[nt][j], o.x);
+                            const float f0 = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mn), f1 = o.x == mn ? 1.f : ex2(o.x - mn);
+                            m[nt][j] = mn;
+                            l[nt][j] = l[nt][j] * f0 + o.y * f1;
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) {
+                                acc[nt][t][j] = acc[nt][t][j] * f0 + ar[r * C::AROW + dim(t, 0)] * f1;
+                                acc[nt][t][2 + j] = acc[nt][t][2 + j] * f0 + ar[r * C::AROW + dim(t, 1)] * f1;
+                            }
+                        }
+                }
+                if (from + 1 < KW) __syncthreads();
+            }
+            const int64_t at = w0 + it;
+            const int64_t first = at - cur.tile;  // the item's first tile in the deal
+            const bool whole = first >= w0 && last;
+            const int rows = min(ROWS, cur.s.n * a.G - cur.rt * ROWS);
+            if (kw == 0) {
+                __syncwarp();
+                put();
+                __syncwarp();
+                const int slot = 2 * blockIdx.x + (first >= w0 ? 1 : 0);
+                for (int r = 0; r < 8 * NTW; ++r) {
+                    const int rt = rw * 8 * NTW + r;
+                    if (rt >= rows) break;
+                    const float2 o = mls[r];
+                    if (whole) {
+                        const int rr = cur.rt * ROWS + rt;
+                        const int64_t row = (int64_t)(cur.s.t0 + rr / a.G) * (a.Hk * a.G) + cur.h * a.G + rr % a.G;
+                        const float f = o.y == 0.f ? 0.f : vs / o.y;
+                        if (D == 128 || lane < 16) {
+                            const float4 x = *reinterpret_cast<const float4*>(ar + r * C::AROW + lane * 4);
+                            *reinterpret_cast<uint2*>(a.out + row * D + lane * 4) =
+                                make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+                        }
+                        if (a.lse && lane == 0)
+                            a.lse[row] = o.y == 0.f ? -INFINITY : (o.x - LIFT + log2f(o.y)) * 0.6931471805599453f;
+                    } else {
+                        const int64_t row = (int64_t)slot * ROWS + rt;
+                        if (D == 128 || lane < 16) {
+                            float4 x = *reinterpret_cast<const float4*>(ar + r * C::AROW + lane * 4);
+                            x.x *= vs; x.y *= vs; x.z *= vs; x.w *= vs;
+                            *reinterpret_cast<float4*>(a.part + row * D + lane * 4) = x;
+                        }
+                        if (lane == 0) a.ml[row] = make_float2(o.x, o.y);
+                    }
+                }
+            }
+            if (it == my - 1 && tid == 0) {
+                int parts = 0;
+                if (!last && first >= w0) parts = (int)((first + cur.n - 1) / per - blockIdx.x) + 1;
+                a.hdr[blockIdx.x] = make_int4(parts, cur.s.t0, cur.rt * ROWS, cur.h);
+                a.hdr_rows[blockIdx.x] = rows;
+            }
+        }
+        if (it + 1 < my) att_next<ROWS, TK>(a, cur);
+    }
+}
+
+// Joins the parts of an item that starts in CTA blockIdx.x and ends in a later
+// one: part 0 in that CTA's second slot, the others in the first slot of the
+// CTAs after it, always in that order.  blockIdx.y takes every gridDim.y-th row;
+// the warps share a row's parts.
+template <int D>
+__global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArgs a, int rows_per, float lift) {
+    constexpr int V = D / 32;
+    __shared__ float s_acc[ATT_JOIN_WARPS][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int4 h = a.hdr[c];
+    if (h.x == 0) return;
+    const int rows = a.hdr_rows[c];
+    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        float top = -INFINITY;
+        for (int p = lane; p < h.x; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int p = lane; p < h.x; p += 32) {
+            const float2 o = a.ml[slot(p) + r];
+            sum += o.y * ex2(o.x - ref);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+        for (int p = warp; p < h.x; p += ATT_JOIN_WARPS) {
+            const int64_t row = slot(p) + r;
+            const float f = ex2(a.ml[row].x - ref);
+            const float* x = a.part + row * D + lane;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += f * x[i * 32];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
+        __syncthreads();
+        const int rr = h.z + r;
+        const int64_t row = (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        if (threadIdx.x < D) {
+            float x = 0.f;
+#pragma unroll
+            for (int w = 0; w < ATT_JOIN_WARPS; ++w) x += s_acc[w][threadIdx.x];
+            a.out[row * D + threadIdx.x] = f32_to_bf16_bits(x * f);
+        }
+        if (a.lse && threadIdx.x == 0)
+            a.lse[row] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
+    }
+}

@@ -9,9 +9,11 @@
 #include <mutex>
 #include <vector>
 
+#include "attention.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 #include "decode_fused.cuh"
+#include "kvcache.cuh"
 #include "perm.cuh"
 #include "prefill.cuh"
 #include "router.cuh"
@@ -934,6 +936,12 @@ int moe_timeout_site(void* stream) {
     return v;
 }
 
+}  // extern "C"
+
+#include "attention_host.cuh"
+
+extern "C" {
+
 #ifdef MOE_PROBE
 // Measurement builds only: the fused decode kernel's phase timestamps of the last launch.
 int moe_probe_read(unsigned long long* host) {
@@ -959,6 +967,7 @@ const char* moe_strerror(int code) {
         case MOE_ERR_CUDA: return "CUDA launch or query failed";
         case MOE_ERR_SLOT: return "a selected expert has no valid arena slot (it contributed zero)";
         case MOE_ERR_TIMEOUT: return "a bounded device-side wait expired";
+        case MOE_ERR_PAGES: return "not enough free pages or table entries for a request's new tokens (it got none)";
         case MOE_ERR_STATIC: return "size beyond the fixed scratch of moe_route_static (T > MOE_ROUTE_STATIC_MAX_T)";
         default: return "unknown error code";
     }
