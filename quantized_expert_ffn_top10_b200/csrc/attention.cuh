@@ -18,7 +18,7 @@
 #include "common.cuh"
 
 #define ATT_MAX_CTAS 304        // 2 x 152: workspace is sized for this many
-#define ATT_PART_ROWS 64        // rows of partial sums per SM and slot (32 x 2 CTAs, or 64)
+#define ATT_PART_ROWS 256       // rows of partial sums per SM and slot
 #define ATT_JOIN_WARPS 8
 
 struct AttnArgs {
@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
 
 // Joins the parts of an item that starts in CTA blockIdx.x and ends in a later
 // one: part 0 in that CTA's second slot, the others in the first slot of the
-// CTAs after it, always in that order.  blockIdx.y takes every gridDim.y-th row;
-// the warps share a row's parts.
+// CTAs after it, always in that order.  A row with few parts is one warp's; the
+// 8 warps of a CTA share a row with many (a long cache and few rows).
 template <int D>
 __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArgs a, int rows_per, float lift) {
     constexpr int V = D / 32;
@@ -722,8 +722,11 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
     const int4 h = a.hdr[c];
     if (h.x == 0) return;
     const int rows = a.hdr_rows[c];
+    const bool few = h.x <= ATT_JOIN_WARPS;
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int r0 = few ? blockIdx.y * ATT_JOIN_WARPS + warp : blockIdx.y;
+    const int step = few ? gridDim.y * ATT_JOIN_WARPS : gridDim.y;
+    for (int r = r0; r < rows; r += step) {
         float top = -INFINITY;
         for (int p = lane; p < h.x; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
 #pragma unroll
@@ -736,31 +739,36 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        const int rr = h.z + r;
+        const int64_t row = (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll 4
-        for (int p = warp; p < h.x; p += ATT_JOIN_WARPS) {
-            const int64_t row = slot(p) + r;
-            const float f = ex2(a.ml[row].x - ref);
-            const float* x = a.part + row * D + lane;
+        for (int p = few ? 0 : warp; p < h.x; p += few ? 1 : ATT_JOIN_WARPS) {
+            const int64_t at = slot(p) + r;
+            const float f = ex2(a.ml[at].x - ref);
+            const float* x = a.part + at * D + lane;
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] += f * x[i * 32];
         }
-        __syncthreads();
+        if (few) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
-        __syncthreads();
-        const int rr = h.z + r;
-        const int64_t row = (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
-        const float f = sum == 0.f ? 0.f : 1.f / sum;
-        if (threadIdx.x < D) {
-            float x = 0.f;
+            for (int i = 0; i < V; ++i) a.out[row * D + lane + i * 32] = f32_to_bf16_bits(acc[i] * inv);
+        } else {
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < ATT_JOIN_WARPS; ++w) x += s_acc[w][threadIdx.x];
-            a.out[row * D + threadIdx.x] = f32_to_bf16_bits(x * f);
+            for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
+            __syncthreads();
+            if (threadIdx.x < D) {
+                float x = 0.f;
+#pragma unroll
+                for (int w = 0; w < ATT_JOIN_WARPS; ++w) x += s_acc[w][threadIdx.x];
+                a.out[row * D + threadIdx.x] = f32_to_bf16_bits(x * inv);
+            }
         }
-        if (a.lse && threadIdx.x == 0)
+        if (a.lse && (few ? lane : threadIdx.x) == 0)
             a.lse[row] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
     }
 }

@@ -92,6 +92,7 @@ cudaError_t attn_attrs() {
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 1, 4>, AttCfg<D, F8, 2, 1, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 4>, AttCfg<D, F8, 2, 2, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 4, 2>, AttCfg<D, F8, 2, 4, 2>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8>, AcCfg<D>::SMEM);
     return e;
 }
 
@@ -111,16 +112,10 @@ int attn_init(int* sms) {
     return MOE_OK;
 }
 
-template <int D, bool F8, int NTW, int RW, int KW>
-cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
-    using C = AttCfg<D, F8, NTW, RW, KW>;
-    static_assert(2 * C::PER_SM * C::ROWS <= 2 * ATT_PART_ROWS, "the workspace holds the partial sums of every CTA");
-    const int grid = std::min(sms * C::PER_SM, ATT_MAX_CTAS * C::PER_SM / 2);
-    k_attn_rows<D, F8, NTW, RW, KW><<<grid, C::NTH, C::SMEM, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+template <int D>
+cudaError_t launch_attn_join(const AttnArgs& a, int grid, int rows, float lift, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, std::min(C::ROWS, 8));
+    cfg.gridDim = dim3(grid, 8);
     cfg.blockDim = dim3(32 * ATT_JOIN_WARPS);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -128,9 +123,26 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<D>, a, C::ROWS, F8 ? 10.f : 0.f);
+    return cudaLaunchKernelEx(&cfg, k_attn_join<D>, a, rows, lift);
 }
 
+template <int D, bool F8, int NTW, int RW, int KW>
+cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
+    using C = AttCfg<D, F8, NTW, RW, KW>;
+    static_assert(2 * C::PER_SM * C::ROWS <= 2 * ATT_PART_ROWS, "the workspace holds the partial sums of every CTA");
+    const int grid = std::min(sms * C::PER_SM, ATT_MAX_CTAS * C::PER_SM / 2);
+    k_attn_rows<D, F8, NTW, RW, KW><<<grid, C::NTH, C::SMEM, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attn_join<D>(a, grid, C::ROWS, F8 ? 10.f : 0.f, st) : e;
+}
+
+template <int D, bool F8>
+cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, cudaStream_t st) {
+    const int grid = std::min(sms, ATT_MAX_CTAS / 2);
+    k_attn_chunk<D, F8><<<grid, AC_THREADS, AcCfg<D>::SMEM, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attn_join<D>(a, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
+}
 // Rows of a request that share a cached head, at most: the row tile that wastes least
 template <int D, bool F8>
 cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
@@ -138,6 +150,7 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     if (rows <= 8) return launch_attn_rows<D, F8, 1, 1, 4>(a, sms, st);
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
     if (rows <= 32) return launch_attn_rows<D, F8, 2, 2, 4>(a, sms, st);
+    if (a.max_q > MOE_DECODE_MAX_T && rows >= 128) return launch_attn_chunk<D, F8>(a, sms, st);
     return launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st);
 }
 

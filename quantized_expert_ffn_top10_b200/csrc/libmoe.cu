@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "attention.cuh"
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "decode.cuh"
 #include "decode_fused.cuh"

@@ -95,15 +95,16 @@ def attn_limits(ref, D, n_keys, e4m3):
     """Bounds of |out - ref| and |lse - ref|, counted in roundings.
 
     out: its own rounding to bf16, 2^-8 of the value; the numerators' rounding
-    to bf16 2^-8 (fp16, e4m3 caches: 2^-11, and 2^-35 of the largest for what
-    falls below fp16's steps) of the weight; the fp32 sum over the keys, each
+    to bf16 2^-8 (fp16, e4m3 caches: 2^-11, and for what falls below fp16's
+    normal steps half of its smallest, 2^-25, with the numerators lifted by 2^6
+    at least: 2^-31 of a numerator's reference for each key) of the weight; the fp32 sum over the keys, each
     step cut or rounded to 2^-23; and a score error ds, which moves every
     softmax weight by at most 2 ds.  ds: D products summed in fp32 at 2^-23 a
     step, scaling and base-2 exponent of the score itself (|s| <= slack) at a
     few 2^-24, and the exponential at 2^-22."""
     out, lse, weight, slack = ref
     ds = (D + 16) * 2.0 ** -23 * slack + 2.0 ** -21
-    p = 2.0 ** -11 + n_keys * 2.0 ** -34 if e4m3 else 2.0 ** -8
+    p = 2.0 ** -11 + n_keys * 2.0 ** -31 if e4m3 else 2.0 ** -8
     lim = 1.01 * (2.0 ** -8 * np.abs(out) + (p + (2 * ds)[..., None] + n_keys * 2.0 ** -22) * weight) + 1e-30
     return lim, ds + n_keys * 2.0 ** -23 + np.where(np.isfinite(lse), np.abs(lse), 0) * 2.0 ** -22
 
