@@ -29,7 +29,7 @@ struct AttnArgs {
     int64_t page_b, token_b, head_b;  // bytes
     int n_pages, page_size;
     const int32_t *cu, *kv_len, *table;
-    int width, T, B, Hk, G, max_q, window;
+    int width, T, B, Hk, G, max_q, window, tma;
     float scale, softcap;
     const float* slopes;
     const int32_t* prefix;
@@ -37,14 +37,29 @@ struct AttnArgs {
     float* lse;
     float* part;   // [2 * CTAs][rows][D]
     float2* ml;    // [2 * CTAs][rows]: exponent reference (base 2) and sum
-    int4* hdr;     // [CTAs]: {parts, first token, row of the request, cached head} of the item cut at this CTA's end
-    int32_t* hdr_rows;
+    int4* hdr;     // [CTAs]: {parts | rows << 16, first token, row of the request, cached head} of the item cut at this CTA's end
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two fp32 at once
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
+    return r;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -118,24 +133,25 @@ struct AttCur {
     AttSeq s;
 };
 
-template <int ROWS, int TK>
+// Key tiles of a row tile; they start at the first visible key, or at the multiple of ALIGN at or before it.
+template <int ROWS, int TK, int ALIGN>
 __device__ __forceinline__ int att_tiles(const AttnArgs& a, const AttSeq& s, int rt, int& lo, int& hi) {
     const int i0 = rt * ROWS / a.G, i1 = min(s.n - 1, (rt * ROWS + ROWS - 1) / a.G);
     int l1, h0;
     att_range(a, s, i0, lo, h0);
     att_range(a, s, i1, l1, hi);
+    lo -= lo % ALIGN;
     return hi > lo ? (hi - lo + TK - 1) / TK : 1;  // a row tile without a key still has its rows to write
 }
 
-template <int ROWS, int TK>
+template <int ROWS, int TK, int ALIGN>
 __device__ __forceinline__ void att_enter(const AttnArgs& a, AttCur& c) {
-    c.n = att_tiles<ROWS, TK>(a, c.s, c.rt, c.lo, c.hi);
+    c.n = att_tiles<ROWS, TK, ALIGN>(a, c.s, c.rt, c.lo, c.hi);
 }
 
-// Next key tile in the deal's order: tiles of an item, cached heads of a row tile, row tiles, requests.
-template <int ROWS, int TK>
-__device__ __forceinline__ void att_next(const AttnArgs& a, AttCur& c) {
-    if (++c.tile < c.n) return;
+// Next item in the deal's order (cached heads of a row tile, row tiles, requests), and next key tile.
+template <int ROWS, int TK, int ALIGN>
+__device__ __forceinline__ void att_next_item(const AttnArgs& a, AttCur& c) {
     c.tile = 0;
     if (++c.h < a.Hk) return;
     c.h = 0;
@@ -146,19 +162,36 @@ __device__ __forceinline__ void att_next(const AttnArgs& a, AttCur& c) {
             c.s = att_seq(a, c.b);
         } while (c.s.n == 0);
     }
-    att_enter<ROWS, TK>(a, c);
+    att_enter<ROWS, TK, ALIGN>(a, c);
 }
 
-// The deal: total tiles, tiles per CTA, and where this CTA starts.  Every CTA
-// computes it for itself, with two block scans: row tiles per request (kept in
-// `base`, B + 1 ints of shared memory), then key tiles per row tile.
-template <int ROWS, int TK, int NTH>
-__device__ void att_deal(const AttnArgs& a, int* base, int64_t* red, AttCur& c, int64_t& w0, int64_t& per, int64_t& total) {
+template <int ROWS, int TK, int ALIGN>
+__device__ __forceinline__ void att_next(const AttnArgs& a, AttCur& c) {
+    if (++c.tile == c.n) att_next_item<ROWS, TK, ALIGN>(a, c);
+}
+
+// The deal: total, share per CTA, and where this CTA starts, in tiles, an item counting OV
+// tiles more than it has (what beginning and ending it costs).  Every CTA computes it for
+// itself: one read of the lengths into shared memory, then two block scans, row tiles per
+// request and key tiles per row tile.  `scratch`: att_deal_bytes(B) of shared memory.
+constexpr __host__ __device__ int att_deal_bytes(int B) { return 16 * B + 4 * (B + 1) + 16 + 8 * 32; }
+
+template <int ROWS, int TK, int NTH, int ALIGN, int OV>
+__device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, AttCur& c, int64_t& w0, int64_t& per, int64_t& total,
+                                         int64_t& start) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int4* const seq = reinterpret_cast<int4*>(scratch);
+    int64_t* const red = reinterpret_cast<int64_t*>(scratch + 16 * a.B);
+    int* const base = reinterpret_cast<int*>(scratch + 16 * a.B + 8 * 32);  // first row tile of each request
     __shared__ int s_b, s_rt;
     __shared__ int64_t s_before;
+    auto get = [&](int b) {
+        const int4 v = seq[b];
+        return AttSeq{v.x, v.y, v.z, v.w};
+    };
     auto scan = [&](int64_t v, int64_t& all) {  // exclusive over the block
         int64_t inc = v;
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t t = __shfl_up_sync(~0u, inc, d);
             if (lane >= d) inc += t;
@@ -168,45 +201,52 @@ __device__ void att_deal(const AttnArgs& a, int* base, int64_t* red, AttCur& c, 
         __syncthreads();
         int64_t ex = inc - v;
         all = 0;
+#pragma unroll
         for (int w = 0; w < NTH / 32; ++w) {
-            if (w < warp) ex += red[w];
-            all += red[w];
+            const int64_t t = red[w];
+            if (w < warp) ex += t;
+            all += t;
         }
         return ex;
     };
     const int ipt = (a.B + NTH - 1) / NTH, b0 = min(a.B, tid * ipt), b1 = min(a.B, b0 + ipt);
     int64_t mine = 0, entries;
-    for (int b = b0; b < b1; ++b) mine += ((int64_t)att_seq(a, b).n * a.G + ROWS - 1) / ROWS;
+    for (int b = b0; b < b1; ++b) {
+        const AttSeq s = att_seq(a, b);
+        seq[b] = make_int4(s.t0, s.n, s.kv, s.pre);
+        mine += ((int64_t)s.n * a.G + ROWS - 1) / ROWS;
+    }
     int64_t ex = scan(mine, entries);
     for (int b = b0; b < b1; ++b) {
         base[b] = (int)ex;
-        ex += ((int64_t)att_seq(a, b).n * a.G + ROWS - 1) / ROWS;
+        ex += ((int64_t)seq[b].y * a.G + ROWS - 1) / ROWS;
     }
     if (tid == 0) base[a.B] = (int)entries;
     __syncthreads();
     const int ept = (int)((entries + NTH - 1) / NTH), e0 = min((int)entries, tid * ept), e1 = min((int)entries, e0 + ept);
-    auto find = [&](int e) {  // the last request that starts at or before entry e
-        int lo = 0, hi = a.B;
-        while (hi - lo > 1) {
+    int first_b = 0;  // the last request that starts at or before entry e0
+    if (e0 < e1)
+        for (int lo = 0, hi = a.B; hi - lo > 1;) {
             const int mid = (lo + hi) >> 1;
-            if (base[mid] <= e) lo = mid;
+            if (base[mid] <= e0) lo = mid;
             else hi = mid;
+            first_b = lo;
         }
-        return lo;
+    // calls f(request, row tile, units) for this thread's entries until it returns true
+    auto each = [&](auto f) {
+        int b = first_b;
+        AttSeq s = get(b);
+        for (int e = e0; e < e1; ++e) {
+            if (e >= base[b + 1]) {
+                do ++b; while (base[b + 1] <= e);
+                s = get(b);
+            }
+            int lo, hi;
+            if (f(b, e - base[b], att_tiles<ROWS, TK, ALIGN>(a, s, e - base[b], lo, hi) + OV)) break;
+        }
     };
-    int64_t tiles = 0;
-    int b = e0 < e1 ? find(e0) : 0;
-    int first_b = b;
-    AttSeq s = att_seq(a, b);
-    int lo, hi;
-    for (int e = e0; e < e1; ++e) {
-        if (e >= base[b + 1]) {
-            do ++b; while (base[b + 1] <= e);
-            s = att_seq(a, b);
-        }
-        tiles += att_tiles<ROWS, TK>(a, s, e - base[b], lo, hi);
-    }
-    int64_t all;
+    int64_t tiles = 0, all;
+    each([&](int, int, int n) { tiles += n; return false; });
     const int64_t before = scan(tiles, all);
     total = all * a.Hk;
     per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)1);
@@ -215,31 +255,26 @@ __device__ void att_deal(const AttnArgs& a, int* base, int64_t* red, AttCur& c, 
         const int64_t at = w0 / a.Hk;  // the entry that holds tile `at` of one head holds w0
         if (at >= before && at < before + tiles) {
             int64_t p = before;
-            b = first_b;
-            s = att_seq(a, b);
-            for (int e = e0; e < e1; ++e) {
-                if (e >= base[b + 1]) {
-                    do ++b; while (base[b + 1] <= e);
-                    s = att_seq(a, b);
+            each([&](int b, int rt, int n) {
+                if (at >= p + n) {
+                    p += n;
+                    return false;
                 }
-                const int n = att_tiles<ROWS, TK>(a, s, e - base[b], lo, hi);
-                if (at < p + n) {
-                    s_b = b;
-                    s_rt = e - base[b];
-                    s_before = p;
-                    break;
-                }
-                p += n;
-            }
+                s_b = b;
+                s_rt = rt;
+                s_before = p;
+                return true;
+            });
         }
         __syncthreads();
         c.b = s_b;
         c.rt = s_rt;
-        c.s = att_seq(a, c.b);
-        att_enter<ROWS, TK>(a, c);
+        c.s = get(c.b);
+        att_enter<ROWS, TK, ALIGN>(a, c);
         const int64_t rem = w0 - s_before * a.Hk;
-        c.h = (int)(rem / c.n);
-        c.tile = (int)(rem % c.n);
+        c.h = (int)(rem / (c.n + OV));
+        start = s_before * a.Hk + (int64_t)c.h * (c.n + OV);
+        c.tile = (int)max(w0 - start - OV, (int64_t)0);
     }
 }
 
@@ -259,7 +294,7 @@ struct AttCfg {
     static constexpr int OFF_ROW = OFF_ML + RW * 8 * NTW * 8, SMEM = OFF_ROW + ST * TK * 8;
     static_assert(TK <= NTH || TK == 128, "one thread looks up one key");
     static_assert(PER_SM * (SMEM + 128 + 1024) <= 233472, "the CTAs of an SM share its 228 KB");
-    static_assert((4097 + 64) * 4 <= OFF_AREA, "the deal's scan borrows the stages");
+    static_assert(att_deal_bytes(MOE_ATTN_MAX_B) <= OFF_AREA, "the deal borrows the stages");
 };
 
 // One warp's share: RW row groups of 8 NTW rows x KW key groups.  The products
@@ -285,9 +320,8 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     AttCur pre;
-    int64_t w0, per, total;
-    att_deal<ROWS, TK, NTH>(a, reinterpret_cast<int*>(smem), reinterpret_cast<int64_t*>(smem + C::OFF_AREA), pre, w0, per,
-                            total);
+    int64_t w0, per, total, start;
+    att_deal<ROWS, TK, NTH, 1, 0>(a, smem, pre, w0, per, total, start);
     const int my = (int)max((int64_t)0, min(per, total - w0));
     if (my == 0) {
         if (tid == 0) a.hdr[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -313,7 +347,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
         }
         if (pre_n < my) {
             ++pre_n;
-            if (pre_n < my) att_next<ROWS, TK>(a, pre);
+            if (pre_n < my) att_next<ROWS, TK, 1>(a, pre);
         }
     };
     auto hand_over = [&](int p) {
@@ -701,39 +735,50 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
             if (it == my - 1 && tid == 0) {
                 int parts = 0;
                 if (!last && first >= w0) parts = (int)((first + cur.n - 1) / per - blockIdx.x) + 1;
-                a.hdr[blockIdx.x] = make_int4(parts, cur.s.t0, cur.rt * ROWS, cur.h);
-                a.hdr_rows[blockIdx.x] = rows;
+                a.hdr[blockIdx.x] = make_int4(parts | rows << 16, cur.s.t0, cur.rt * ROWS, cur.h);
             }
         }
-        if (it + 1 < my) att_next<ROWS, TK>(a, cur);
+        if (it + 1 < my) att_next<ROWS, TK, 1>(a, cur);
     }
 }
 
 // Joins the parts of an item that starts in CTA blockIdx.x and ends in a later
 // one: part 0 in that CTA's second slot, the others in the first slot of the
-// CTAs after it, always in that order.  A row with few parts is one warp's; the
-// 8 warps of a CTA share a row with many (a long cache and few rows).
+// CTAs after it, always in that order.  A row with up to 32 parts is one warp's;
+// the 8 warps of a CTA share a row with more (a long cache and few rows).
+// Bound by latency: the first parts of a row are asked for before their weights.
 template <int D>
 __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArgs a, int rows_per, float lift) {
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, AHEAD = 8;
     __shared__ float s_acc[ATT_JOIN_WARPS][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int4 h = a.hdr[c];
-    if (h.x == 0) return;
-    const int rows = a.hdr_rows[c];
-    const bool few = h.x <= ATT_JOIN_WARPS;
+    const int parts = h.x & 0xffff, rows = h.x >> 16;
+    if (parts == 0) return;
+    const bool few = parts <= 32;
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
+    const int p0 = few ? 0 : warp, dp = few ? 1 : ATT_JOIN_WARPS;  // this warp's parts of a row
     const int r0 = few ? blockIdx.y * ATT_JOIN_WARPS + warp : blockIdx.y;
     const int step = few ? gridDim.y * ATT_JOIN_WARPS : gridDim.y;
     for (int r = r0; r < rows; r += step) {
+        float x[AHEAD][V];
+        auto load = [&](int first) {
+#pragma unroll
+            for (int n = 0; n < AHEAD; ++n) {
+                const int p = first + n * dp;
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[n][i] = p < parts ? a.part[(slot(p) + r) * D + i * 32 + lane] : 0.f;
+            }
+        };
+        load(p0);
         float top = -INFINITY;
-        for (int p = lane; p < h.x; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
+        for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
         const float ref = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
-        for (int p = lane; p < h.x; p += 32) {
+        for (int p = lane; p < parts; p += 32) {
             const float2 o = a.ml[slot(p) + r];
             sum += o.y * ex2(o.x - ref);
         }
@@ -745,13 +790,16 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int p = few ? 0 : warp; p < h.x; p += few ? 1 : ATT_JOIN_WARPS) {
-            const int64_t at = slot(p) + r;
-            const float f = ex2(a.ml[at].x - ref);
-            const float* x = a.part + at * D + lane;
+        for (int first = p0; first < parts; first += AHEAD * dp) {
+            if (first > p0) load(first);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += f * x[i * 32];
+            for (int n = 0; n < AHEAD; ++n) {
+                const int p = first + n * dp;
+                if (p >= parts) break;
+                const float f = ex2(a.ml[slot(p) + r].x - ref);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += f * x[n][i];
+            }
         }
         if (few) {
 #pragma unroll
@@ -762,10 +810,10 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
             for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
             __syncthreads();
             if (threadIdx.x < D) {
-                float x = 0.f;
+                float y = 0.f;
 #pragma unroll
-                for (int w = 0; w < ATT_JOIN_WARPS; ++w) x += s_acc[w][threadIdx.x];
-                a.out[row * D + threadIdx.x] = f32_to_bf16_bits(x * inv);
+                for (int w = 0; w < ATT_JOIN_WARPS; ++w) y += s_acc[w][threadIdx.x];
+                a.out[row * D + threadIdx.x] = f32_to_bf16_bits(y * inv);
             }
         }
         if (a.lse && (few ? lane : threadIdx.x) == 0)

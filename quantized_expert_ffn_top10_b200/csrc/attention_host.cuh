@@ -32,7 +32,7 @@ inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
 // ---------------------------------------------------------------- attention
 
 struct AttnWs {
-    size_t hdr, rows, ml, part, total;
+    size_t hdr, ml, part, total;
 };
 
 AttnWs attn_ws(int D) {
@@ -41,7 +41,6 @@ AttnWs attn_ws(int D) {
     auto put = [&](size_t bytes) { size_t r = o; o += al(bytes); return r; };
     const size_t slots = (size_t)ATT_MAX_CTAS * ATT_PART_ROWS;  // 2 x CTAs x rows of the widest kernel at 2 CTAs per SM
     w.hdr = put(ATT_MAX_CTAS * sizeof(int4));
-    w.rows = put(ATT_MAX_CTAS * 4);
     w.ml = put(slots * sizeof(float2));
     w.part = put(slots * D * 4);
     w.total = o;
@@ -92,7 +91,7 @@ cudaError_t attn_attrs() {
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 1, 4>, AttCfg<D, F8, 2, 1, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 4>, AttCfg<D, F8, 2, 2, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 4, 2>, AttCfg<D, F8, 2, 4, 2>::SMEM);
-    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8>, AcCfg<D>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8>, AcCfg<D, F8>::SMEM);
     return e;
 }
 
@@ -112,10 +111,29 @@ int attn_init(int* sms) {
     return MOE_OK;
 }
 
+// A cache as a 4-D tensor (element, token, head, page); a box is min(page, 128)
+// tokens of one head of one page, 64 bf16 columns with the 128-byte swizzle or a
+// whole e4m3 row without one.  False for pages that such boxes do not tile.
+template <int D, bool F8>
+bool tmap_cache(CUtensorMap* m, const uint8_t* base, const AttnArgs& a) {
+    const int ps = a.page_size;
+    if (ps < 8 || (ps & (ps - 1)) || !encoder()) return false;
+    cuuint64_t dims[4] = {D, (cuuint64_t)ps, (cuuint64_t)a.Hk, (cuuint64_t)a.n_pages};
+    // a dimension of one element has no stride to speak of
+    cuuint64_t strides[3] = {(cuuint64_t)a.token_b, (cuuint64_t)(a.Hk > 1 ? a.head_b : 16), (cuuint64_t)(a.n_pages > 1 ? a.page_b : 16)};
+    for (const cuuint64_t s : strides)
+        if (s == 0 || s >= (1ull << 40)) return false;
+    cuuint32_t box[4] = {F8 ? D : 64, (cuuint32_t)std::min(ps, AC_TK), 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return encoder()(m, F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t*>(base), dims,
+                     strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, F8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_attn_join(const AttnArgs& a, int grid, int rows, float lift, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, 8);
+    cfg.gridDim = dim3(grid, std::min(rows, 32));
     cfg.blockDim = dim3(32 * ATT_JOIN_WARPS);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -137,9 +155,11 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
 }
 
 template <int D, bool F8>
-cudaError_t launch_attn_chunk(const AttnArgs& a, int sms, cudaStream_t st) {
+cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     const int grid = std::min(sms, ATT_MAX_CTAS / 2);
-    k_attn_chunk<D, F8><<<grid, AC_THREADS, AcCfg<D>::SMEM, st>>>(a);
+    CUtensorMap tk{}, tv{};
+    a.tma = tmap_cache<D, F8>(&tk, a.k, a) && tmap_cache<D, F8>(&tv, a.v, a);
+    k_attn_chunk<D, F8><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }
@@ -150,7 +170,7 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     if (rows <= 8) return launch_attn_rows<D, F8, 1, 1, 4>(a, sms, st);
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
     if (rows <= 32) return launch_attn_rows<D, F8, 2, 2, 4>(a, sms, st);
-    if (a.max_q > MOE_DECODE_MAX_T && rows >= 128) return launch_attn_chunk<D, F8>(a, sms, st);
+    if (rows >= 128) return launch_attn_chunk<D, F8>(a, sms, st);
     return launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st);
 }
 
@@ -172,7 +192,6 @@ int run_attn(const AttnCall& c) {
     a.scale = c.scale; a.softcap = c.softcap; a.slopes = c.slopes; a.prefix = c.prefix;
     a.out = c.out; a.lse = c.lse;
     a.hdr = reinterpret_cast<int4*>(c.ws + L.hdr);
-    a.hdr_rows = reinterpret_cast<int32_t*>(c.ws + L.rows);
     a.ml = reinterpret_cast<float2*>(c.ws + L.ml);
     a.part = reinterpret_cast<float*>(c.ws + L.part);
     cudaError_t e;

@@ -68,26 +68,29 @@ def attn_ref(q, keys, values, q_len, kv_len, scale, softcap=0.0, window=0, slope
         kv = int(kv_len[b])
         K, V = np.asarray(keys[b], np.float64), np.asarray(values[b], np.float64)
         G = Hq // K.shape[1]
-        j = np.arange(kv)
-        for i in range(n):
-            pos = kv - n + i
-            hi = max(pos + 1, 0 if prefix is None else min(int(prefix[b]), kv), 0)
-            lo = max(0, pos - window + 1) if window else 0
-            if hi > lo:
-                for h in range(Hq):
-                    k, v = K[lo:hi, h // G], V[lo:hi, h // G]
-                    s = k @ q[t, h] * scale
-                    slack[t, h] = (np.abs(k) @ np.abs(q[t, h])).max() * abs(scale)
-                    if softcap:
-                        s = softcap * np.tanh(s / softcap)
-                    if slopes is not None:
-                        s = s - float(slopes[h]) * np.abs(pos - j[lo:hi])
-                    m = s.max()
-                    e = np.exp(s - m)
-                    out[t, h] = e @ v / e.sum()
-                    weight[t, h] = e @ np.abs(v) / e.sum()
-                    lse[t, h] = m + math.log(e.sum())
-            t += 1
+        pos, j = kv - n + np.arange(n)[:, None], np.arange(kv)[None]
+        hi = np.maximum(pos + 1, 0 if prefix is None else min(int(prefix[b]), kv))
+        seen = (j < hi) & ((j > pos - window) if window else True)
+        rows = np.flatnonzero(seen.any(1))  # the others keep 0 and -inf
+        if rows.size:
+            sl = t + rows
+            for h in range(Hq):
+                k, v, qq = K[:, h // G], V[:, h // G], q[sl, h]
+                s = qq @ k.T * scale
+                mask = seen[rows]
+                slack[sl, h] = np.where(mask, np.abs(qq) @ np.abs(k).T, 0).max(1) * abs(scale)
+                if softcap:
+                    s = softcap * np.tanh(s / softcap)
+                if slopes is not None:
+                    s = s - float(slopes[h]) * np.abs(pos[rows] - j)
+                s = np.where(mask, s, -np.inf)
+                m = s.max(1, keepdims=True)
+                e = np.exp(s - m)
+                tot = e.sum(1, keepdims=True)
+                out[sl, h] = e @ v / tot
+                weight[sl, h] = e @ np.abs(v) / tot
+                lse[sl, h] = (m + np.log(tot))[:, 0]
+        t += n
     return out, lse, weight, slack
 
 

@@ -113,6 +113,9 @@ CHUNKS = [
     dict(q_len=[200], kv_len=[90], Hq=3, Hk=3, D=64),              # rows before the first key
     dict(q_len=[300, 17], kv_len=[1300, 17], Hq=8, Hk=1, page=64),
     dict(q_len=[257], kv_len=[257], Hq=16, Hk=2, page=1),
+    dict(q_len=[1500], kv_len=[2900], Hq=16, Hk=2, page=64),       # several items, and cut ones, in every CTA
+    dict(q_len=[700, 900, 11], kv_len=[700, 2222, 2000], Hq=12, Hk=4, D=64, page=16, head_major=True),
+    dict(q_len=[500, 40], kv_len=[1500, 3000], Hq=8, Hk=2, page=24),
 ]
 
 
