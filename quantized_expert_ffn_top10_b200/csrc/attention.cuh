@@ -201,7 +201,7 @@ __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, At
         __syncthreads();
         int64_t ex = inc - v;
         all = 0;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < NTH / 32; ++w) {
             const int64_t t = red[w];
             if (w < warp) ex += t;

@@ -212,21 +212,27 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             const float vs = (F8 && a.v_scale) ? __ldg(a.v_scale + cur.h) : 1.f;
             const bool simple = a.softcap == 0.f && !a.slopes && a.scale * ks > 0.f;  // scores are S times a positive number
             const float slope = (a.slopes && mine) ? __ldg(a.slopes + head) * LOG2E : 0.f;
-            // ---- Q: this warp's 32 rows into the half's K-major operand tile, LPR lanes to a row
+            // ---- Q: this warp's 32 rows into the half's K-major operand tile, LPR lanes to a row.  The loops
+            // that run once an item are kept short: unrolled, they cost more in instruction fetches.
             constexpr int LPR = D / 8, RPI = 32 / LPR;
             float unit = 1.f;
             {
                 const int64_t off = mine ? (int64_t)(cur.s.t0 + i) * a.q_stride + head * D : -1;
-                uint4 w[LPR];
-#pragma unroll
+                uint8_t* const q_w = q_s + (warp & 3) * 32 * 128;
+#pragma unroll 1
                 for (int n = 0; n < LPR; ++n) {
-                    const int64_t o = __shfl_sync(~0u, off, n * RPI + lane / LPR);
-                    w[n] = o >= 0 ? *reinterpret_cast<const uint4*>(a.q + o + (lane % LPR) * 8) : make_uint4(0, 0, 0, 0);
+                    const int q = n * RPI + lane / LPR;
+                    const int64_t o = __shfl_sync(~0u, off, q);
+                    cp_async16(smem_u32(q_w + place(q, lane % LPR)), a.q + (o < 0 ? 0 : o) + (lane % LPR) * 8, o >= 0);
                 }
-#pragma unroll
-                for (int n = 0; n < LPR; ++n) {
-                    if constexpr (F8) {  // the row's largest element to [2^14, 2^15), all of them to fp16
-                        uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                cp_async_commit();
+                cp_async_wait<0>();
+                if constexpr (F8) {  // the row's largest element to [2^14, 2^15), all of them to fp16
+#pragma unroll 2
+                    for (int n = 0; n < LPR; ++n) {
+                        uint4* const at = reinterpret_cast<uint4*>(q_w + place(n * RPI + lane / LPR, lane % LPR));
+                        const uint4 w = *at;
+                        uint32_t x[4] = {w.x, w.y, w.z, w.w};
                         uint32_t top = 0;  // magnitudes of bf16 values compare as integers
 #pragma unroll
                         for (int e = 0; e < 4; ++e) top = max(top, max(x[e] << 16 & 0x7fffffffu, x[e] & 0x7fff0000u));
@@ -238,11 +244,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             x[e] = pack_f16x2(__uint_as_float(x[e] << 16) * down, __uint_as_float(x[e] & 0xffff0000u) * down);
-                        w[n] = make_uint4(x[0], x[1], x[2], x[3]);
+                        *at = make_uint4(x[0], x[1], x[2], x[3]);
                         const float mine_up = __shfl_sync(~0u, up, (lane % RPI) * LPR);
                         if (lane / RPI == n) unit = mine_up;
                     }
-                    *reinterpret_cast<uint4*>(q_s + place((warp & 3) * 32 + n * RPI + lane / LPR, lane % LPR)) = w[n];
                 }
             }
             fence_proxy_async_smem();
@@ -260,22 +265,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     tc_fence_after();
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
                     const bool masked = __any_sync(~0u, k0 < lo || k0 + AC_TK > hi), edit = masked || !simple;
-                    // S is read twice, 64 columns at a time: once for the maximum (scores that are not S
-                    // times a number, or hidden, are written back), once for the numerators
+                    // S is read twice: once for the maximum (scores that are not S times a number, or hidden, are
+                    // written back), once for the numerators
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (edit) {
+                        const int f = masked ? lo - k0 : -1024, e = masked ? hi - k0 : 1024;  // visible columns [f, e)
+                        const float p0 = (float)(pos - k0);
+#pragma unroll 1
+                        for (int g = 0; g < 128; g += 16) {
+                            uint32_t u[16];
+                            tmem_ld16(t_s + g, u);
+                            tmem_ld_wait16(u);
 #pragma unroll
-                    for (int g = 0; g < 128; g += 64) {
-                        uint32_t u[64];
-                        tmem_ld32(t_s + g, u);
-                        tmem_ld32(t_s + g + 32, u + 32);
-                        tmem_ld_wait();
-                        reg_tie32(u);
-                        reg_tie32(u + 32);
-                        if (edit) {
-                            const int f = masked ? lo - k0 - g : -1024, e = masked ? hi - k0 - g : 1024;  // visible columns [f, e)
-                            const float p0 = (float)(pos - k0 - g);
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) {
+                            for (int c = 0; c < 16; ++c) {
                                 float x = __uint_as_float(u[c]);
                                 if (!simple) {
                                     x *= rs;
@@ -283,15 +285,27 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                                         const float y = ex2(x * cap_in);
                                         x = cap_out * (1.f - __fdividef(2.f, 1.f + y));
                                     }
-                                    x -= slope * fabsf(p0 - (float)c);
+                                    x -= slope * fabsf(p0 - (float)(g + c));
                                 }
-                                u[c] = c >= f && c < e ? __float_as_uint(x) : 0xff800000u;
+                                x = g + c >= f && g + c < e ? x : -INFINITY;
+                                t4[c & 3] = fmaxf(t4[c & 3], x);
+                                u[c] = __float_as_uint(x);
                             }
-                            tmem_st32(t_s + g, u);
-                            tmem_st32(t_s + g + 32, u + 32);
+                            tmem_st16(t_s + g, u);
                         }
+                        tmem_st_wait();
+                    } else {
+#pragma unroll 1
+                        for (int g = 0; g < 128; g += 64) {
+                            uint32_t u[64];
+                            tmem_ld32(t_s + g, u);
+                            tmem_ld32(t_s + g + 32, u + 32);
+                            tmem_ld_wait();
+                            reg_tie32(u);
+                            reg_tie32(u + 32);
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(u[c]));
+                            for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(u[c]));
+                        }
                     }
                     const float mul = simple ? rs : 1.f;
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
@@ -312,12 +326,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             }
                         }
                     }
-                    if (edit) tmem_st_wait();
                     const float ref = m == -INFINITY ? 0.f : m - LIFT;
                     // numerators, their sum unrounded, and their 16-bit form over columns of S already read
                     const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
                     float2 la = make_float2(0.f, 0.f), lb = la;
-#pragma unroll
+#pragma unroll 1
                     for (int g = 0; g < 128; g += 64) {
                         uint32_t u[64];
                         tmem_ld32(t_s + g, u);
