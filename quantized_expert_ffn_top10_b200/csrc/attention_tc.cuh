@@ -23,6 +23,8 @@
 // do not tile (not a power of two, or below 8).
 #pragma once
 
+#include <type_traits>
+
 #include "attention.cuh"
 
 #define AC_THREADS 512
@@ -44,6 +46,13 @@ struct AcCfg {
     static_assert(SMEM <= 232448, "227 KB of shared memory per CTA");
 };
 
+// One lane of the warp, the same each time; true for it.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+    return ok != 0;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -54,22 +63,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void reg_tie8(uint32_t* r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
 }
 // no use of these registers is scheduled before this point (after a wait for the loads)
 __device__ __forceinline__ void reg_tie32(uint32_t* r) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                          "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
+    for (int i = 0; i < 32; i += 8) reg_tie8(r + i);
 }
 
 // 4D tiled bulk tensor load global -> shared; c0 is the innermost coordinate (elements).
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 
     if (warp < 8) {
         // ------------------------------------------------ softmax, one thread per row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int half = warp >> 2, r = tid & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), t_s = lanes + S_COL + half * 128,
                        t_o = lanes + O_COL + half * D;
@@ -265,9 +275,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     tc_fence_after();
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
                     const bool masked = __any_sync(~0u, k0 < lo || k0 + AC_TK > hi), edit = masked || !simple;
-                    // S is read twice: once for the maximum (scores that are not S times a number, or hidden, are
-                    // written back), once for the numerators
-                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    // scores that are not S times a number, or hidden ones, are put in S's place first
                     if (edit) {
                         const int f = masked ? lo - k0 : -1024, e = masked ? hi - k0 : 1024;  // visible columns [f, e)
                         const float p0 = (float)(pos - k0);
@@ -287,26 +295,22 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                                     }
                                     x -= slope * fabsf(p0 - (float)(g + c));
                                 }
-                                x = g + c >= f && g + c < e ? x : -INFINITY;
-                                t4[c & 3] = fmaxf(t4[c & 3], x);
-                                u[c] = __float_as_uint(x);
+                                u[c] = g + c >= f && g + c < e ? __float_as_uint(x) : 0xff800000u;  // -inf
                             }
                             tmem_st16(t_s + g, u);
                         }
                         tmem_st_wait();
-                    } else {
-#pragma unroll 1
-                        for (int g = 0; g < 128; g += 64) {
-                            uint32_t u[64];
-                            tmem_ld32(t_s + g, u);
-                            tmem_ld32(t_s + g + 32, u + 32);
-                            tmem_ld_wait();
-                            reg_tie32(u);
-                            reg_tie32(u + 32);
-#pragma unroll
-                            for (int c = 0; c < 64; ++c) t4[c & 3] = fmaxf(t4[c & 3], __uint_as_float(u[c]));
-                        }
                     }
+                    uint32_t u[128];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) tmem_ld32(t_s + g * 32, u + g * 32);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) reg_tie32(u + g * 32);
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2)
+                        t4[(c >> 1) & 3] = fmaxf(t4[(c >> 1) & 3], fmaxf(__uint_as_float(u[c]), __uint_as_float(u[c + 1])));
                     const float mul = simple ? rs : 1.f;
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
                     const bool grew = top > m + GROW || (m == -INFINITY && top > m);
@@ -316,43 +320,34 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         l *= f;
                         if (n > 0) {  // O holds sums already
 #pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(t_o + c, o);
-                                tmem_ld_wait16(o);
+                            for (int c = 0; c < D; c += 8) {
+                                uint32_t o[8];
+                                tmem_ld8(t_o + c, o);
+                                tmem_ld_wait();
+                                reg_tie8(o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st16(t_o + c, o);
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st8(t_o + c, o);
                             }
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m - LIFT;
-                    // numerators, their sum unrounded, and their 16-bit form over columns of S already read
+                    // numerators, their sum unrounded, and their 16-bit form over S
                     const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
                     float2 la = make_float2(0.f, 0.f), lb = la;
-#pragma unroll 1
-                    for (int g = 0; g < 128; g += 64) {
-                        uint32_t u[64];
-                        tmem_ld32(t_s + g, u);
-                        tmem_ld32(t_s + g + 32, u + 32);
-                        tmem_ld_wait();
-                        reg_tie32(u);
-                        reg_tie32(u + 32);
 #pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2) {
-                            uint32_t p[16];
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t p[16];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                float2 x = fma2(make_float2(__uint_as_float(u[q2 * 32 + 2 * c]), __uint_as_float(u[q2 * 32 + 2 * c + 1])),
-                                                mul2, ref2);
-                                x.x = ex2(x.x);
-                                x.y = ex2(x.y);
-                                if (c & 1) lb = add2(lb, x);
-                                else la = add2(la, x);
-                                p[c] = F8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
-                            }
-                            tmem_st16(t_s + g / 2 + q2 * 16, p);
+                        for (int c = 0; c < 16; ++c) {
+                            float2 x = fma2(make_float2(__uint_as_float(u[g * 32 + 2 * c]), __uint_as_float(u[g * 32 + 2 * c + 1])), mul2, ref2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            if (c & 1) lb = add2(lb, x);
+                            else la = add2(la, x);
+                            p[c] = F8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
                         }
+                        tmem_st16(t_s + g * 16, p);
                     }
                     la = add2(la, lb);
                     l += la.x + la.y;
@@ -412,50 +407,59 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         }
                         f = !whole ? vs : l == 0.f ? 0.f : vs / l;
                     }
+                    // FIX: non-finite values in masked tiles were taken out of the product; back to the rows that see them
+                    auto columns = [&](auto fix_tag) {
+                        constexpr bool FIX = decltype(fix_tag)::value;
 #pragma unroll 1
-                    for (int c = 0; c < D / 2; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(t_o + c0 + c, o);
-                        tmem_ld_wait16(o);
-                        float x[16];
+                        for (int c = 0; c < D / 2; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + c0 + c, o);
+                            tmem_ld_wait16(o);
+                            float x[16];
+                            if (two) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            x[e] = two ? __uint_as_float(o[e]) * f0 + other[(c + e) * 128 + r] * f1 : __uint_as_float(o[e]);
-                        if (fix && mine) {
-                            // non-finite values in masked tiles were taken out of the product: back to the rows that see them
-                            int all_lo, all_hi;
-                            seen_by_all(all_lo, all_hi);
-                            for (int j = 0; j < cnt; ++j) {
-                                const int k0 = cur.lo + (cur.tile + j) * AC_TK;
-                                if (k0 >= all_lo && k0 + AC_TK <= all_hi) continue;
-                                for (int key = max(k0, lo); key < min(k0 + AC_TK, hi); ++key) {
-                                    const int col = key / a.page_size, pg = __ldg(a.table + (int64_t)cur.b * a.width + col);
-                                    if (pg < 0 || pg >= a.n_pages) continue;
-                                    const uint8_t* vp = a.v + pg * a.page_b + (int64_t)(key - col * a.page_size) * a.token_b +
-                                                        cur.h * a.head_b;
+                                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]) * f0 + other[(c + e) * 128 + r] * f1;
+                            } else {
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) {
-                                        float y;
-                                        if constexpr (F8) y = half_bits_to_f32((uint16_t)e4m3x2_to_f16x2(vp[c0 + c + e]));
-                                        else y = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(vp)[c0 + c + e]);
-                                        if (!(fabsf(y) < INFINITY)) x[e] += y;
+                                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[e]);
+                            }
+                            if constexpr (FIX) {
+                                int all_lo, all_hi;
+                                seen_by_all(all_lo, all_hi);
+                                for (int j = 0; j < cnt; ++j) {
+                                    const int k0 = cur.lo + (cur.tile + j) * AC_TK;
+                                    if (k0 >= all_lo && k0 + AC_TK <= all_hi) continue;
+                                    for (int key = max(k0, lo); key < min(k0 + AC_TK, hi); ++key) {
+                                        const int col = key / a.page_size, pg = __ldg(a.table + (int64_t)cur.b * a.width + col);
+                                        if (pg < 0 || pg >= a.n_pages) continue;
+                                        const uint8_t* vp = a.v + pg * a.page_b + (int64_t)(key - col * a.page_size) * a.token_b +
+                                                            cur.h * a.head_b;
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) {
+                                            float y;
+                                            if constexpr (F8) y = half_bits_to_f32((uint16_t)e4m3x2_to_f16x2(vp[c0 + c + e]));
+                                            else y = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(vp)[c0 + c + e]);
+                                            if (!(fabsf(y) < INFINITY)) x[e] += y;
+                                        }
                                     }
                                 }
                             }
-                        }
-                        if (whole) {
+                            if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<uint4*>(smem + place(r, c / 8 + e) + half * TILE) =
-                                    make_uint4(pack_bf16x2(x[8 * e] * f, x[8 * e + 1] * f), pack_bf16x2(x[8 * e + 2] * f, x[8 * e + 3] * f),
-                                               pack_bf16x2(x[8 * e + 4] * f, x[8 * e + 5] * f), pack_bf16x2(x[8 * e + 6] * f, x[8 * e + 7] * f));
-                        } else {
+                                for (int e = 0; e < 2; ++e)
+                                    *reinterpret_cast<uint4*>(q_s + place(r, c / 8 + e)) = make_uint4(
+                                        pack_bf16x2(x[8 * e] * f, x[8 * e + 1] * f), pack_bf16x2(x[8 * e + 2] * f, x[8 * e + 3] * f),
+                                        pack_bf16x2(x[8 * e + 4] * f, x[8 * e + 5] * f), pack_bf16x2(x[8 * e + 6] * f, x[8 * e + 7] * f));
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<float4*>(smem + place(r, c / 4 + e) + half * TILE) =
-                                    make_float4(x[4 * e] * f, x[4 * e + 1] * f, x[4 * e + 2] * f, x[4 * e + 3] * f);
+                                for (int e = 0; e < 4; ++e)
+                                    *reinterpret_cast<float4*>(q_s + place(r, c / 4 + e)) =
+                                        make_float4(x[4 * e] * f, x[4 * e + 1] * f, x[4 * e + 2] * f, x[4 * e + 3] * f);
+                            }
                         }
-                    }
+                    };
+                    if (__any_sync(~0u, fix && mine)) columns(std::true_type{});
+                    else columns(std::false_type{});
                     __syncwarp();
                     const int wr = (warp & 3) * 32;  // the warp's rows, so many lanes to each
                     if (whole) {
@@ -466,7 +470,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             const int64_t to = __shfl_sync(~0u, row, q);
                             if (row0 + wr + q < rows)
                                 *reinterpret_cast<uint4*>(a.out + to * D + c0 + (lane % L) * 8) =
-                                    *reinterpret_cast<const uint4*>(smem + place(wr + q, lane % L) + half * TILE);
+                                    *reinterpret_cast<const uint4*>(q_s + place(wr + q, lane % L));
                         }
                     } else {
                         constexpr int L = D / 8;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             const int q = n * (32 / L) + lane / L;
                             if (row0 + wr + q < rows)
                                 *reinterpret_cast<uint4*>(a.part + (prow - lane + q) * D + c0 + (lane % L) * 4) =
-                                    *reinterpret_cast<const uint4*>(smem + place(wr + q, lane % L) + half * TILE);
+                                    *reinterpret_cast<const uint4*>(q_s + place(wr + q, lane % L));
                         }
                     }
                     __syncwarp();
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         }
     } else if (warp < 12) {
         // ------------------------------------------------ widening, cleaning, or the whole gather
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int t = tid - 256;
         constexpr int CHG = D * (F8 ? 1 : 2) / 16, STEP = 128 / CHG;  // 16-byte pieces of a cached row; rows a pass
         const int c = t % CHG, t_row = t / CHG;
@@ -646,8 +650,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp == 12 && lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 12 && elect_one()) {
             // -------------------------------------------- MMAs, one thread
             constexpr uint32_t ID_QK = ac_idesc(F8 ? 0 : 1, AC_TK, false), ID_PV = ac_idesc(F8 ? 0 : 1, D, true);
             const uint32_t sq = smem_u32(smem), ring = sq + C::OFF_RING;
@@ -675,10 +679,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         if (duo || h == 0) ok = mbar_wait_fast(full + ks, k_ph, 25, ks);
                         if (!ok) break;
                         tc_fence_after();
+                        // (addresses count in 16 bytes; rolled loops, or the descriptors are kept in registers)
+                        uint64_t da = make_sdesc_sw128(sq + h * TILE), db = make_sdesc_sw128(ring + ks * TILE);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
-                            tc_mma_bf16(tmem + S_COL + h * 128, make_sdesc_sw128(sq + h * TILE + (k >> 2) * BLK + (k & 3) * 32),
-                                        make_sdesc_sw128(ring + ks * TILE + (k >> 2) * BLK + (k & 3) * 32), ID_QK, k > 0);
+                            tc_mma_bf16(tmem + S_COL + h * 128, da + (k >> 2) * (BLK / 16) + (k & 3) * 2, db + (k >> 2) * (BLK / 16) + (k & 3) * 2, ID_QK, k > 0);
                         tc_commit(sfull + h);
                         if (duo || h == 1) {
                             tc_commit(empty + ks);
@@ -693,10 +698,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         p_ph[h] ^= 1;
                         tc_fence_after();
                         const bool add = duo ? j > 1 : j > 0;
+                        uint64_t dv = make_sdesc_v(ring + vsl * TILE);
 #pragma unroll
                         for (int k = 0; k < AC_TK / 16; ++k)
-                            tc_mma_bf16_ts(tmem + O_COL + h * D, tmem + S_COL + h * 128 + k * 8,
-                                           make_sdesc_v(ring + vsl * TILE + k * 2048), ID_PV, add || k > 0);
+                            tc_mma_bf16_ts(tmem + O_COL + h * D, tmem + S_COL + h * 128 + k * 8, dv + k * 128, ID_PV, add || k > 0);
                         if (duo || h == 1) {
                             tc_commit(empty + vsl);
                             next2(vsl, v_ph);
