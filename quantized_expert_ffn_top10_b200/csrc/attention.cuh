@@ -179,6 +179,22 @@ constexpr __host__ __device__ int att_deal_bytes(int B) { return 16 * B + 4 * (B
 template <int ROWS, int TK, int NTH, int ALIGN, int OV>
 __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, AttCur& c, int64_t& w0, int64_t& per, int64_t& total,
                                          int64_t& start) {
+    if (a.B == 1 && (int64_t)min(a.T, a.max_q) * a.G <= ROWS) {  // one row tile at most: nothing to scan
+        c.b = c.rt = 0;
+        c.s = att_seq(a, 0);
+        total = 0;
+        per = 1;
+        w0 = blockIdx.x;
+        if (c.s.n == 0) return;
+        att_enter<ROWS, TK, ALIGN>(a, c);
+        total = (int64_t)(c.n + OV) * a.Hk;
+        per = (total + gridDim.x - 1) / gridDim.x;
+        w0 = per * blockIdx.x;
+        c.h = (int)(w0 / (c.n + OV));
+        start = (int64_t)c.h * (c.n + OV);
+        c.tile = (int)max(w0 - start - OV, (int64_t)0);
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int4* const seq = reinterpret_cast<int4*>(scratch);
     int64_t* const red = reinterpret_cast<int64_t*>(scratch + 16 * a.B);
@@ -744,9 +760,10 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
 
 // Joins the parts of an item that starts in CTA blockIdx.x and ends in a later
 // one: part 0 in that CTA's second slot, the others in the first slot of the
-// CTAs after it, always in that order.  A row with up to 32 parts is one warp's;
-// the 8 warps of a CTA share a row with more (a long cache and few rows).
-// Bound by latency: the first parts of a row are asked for before their weights.
+// CTAs after it, always in that order.  Rows with up to 8 parts go four to a warp
+// (an item cut once or twice), a row with up to 32 is one warp's, and the 8 warps
+// of a CTA share a row with more (a long cache and few rows).  Bound by latency:
+// the first parts of a row are asked for before their weights.
 template <int D>
 __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArgs a, int rows_per, float lift) {
     constexpr int V = D / 32, AHEAD = 8;
@@ -758,6 +775,54 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
     if (parts == 0) return;
     const bool few = parts <= 32;
     auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
+    auto out_row = [&](int r) {
+        const int rr = h.z + r;
+        return (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
+    };
+    if (parts <= 8) {
+        constexpr int L = D / 4, AT = 32 / L, N = 4 / AT;  // lanes a row, rows at a time, times
+        const int q = lane >> 3, p8 = lane & 7;            // this lane's row and part of the 4 x 8 weights
+        for (int r0 = (blockIdx.y * ATT_JOIN_WARPS + warp) * 4; r0 < rows; r0 += gridDim.y * ATT_JOIN_WARPS * 4) {
+            const bool live = p8 < parts && r0 + q < rows;
+            const float2 o = live ? a.ml[slot(p8) + r0 + q] : make_float2(-INFINITY, 0.f);
+            float4 x[N][2];
+            auto load = [&](int n, int p) {
+                const int r = r0 + n * AT + lane / L;
+                return p < parts && r < rows ? *reinterpret_cast<const float4*>(a.part + (slot(p) + r) * D + (lane % L) * 4)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                x[n][0] = load(n, 0);
+                x[n][1] = load(n, 1);
+            }
+            float top = o.x;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const float w = ex2(o.x - (top == -INFINITY ? 0.f : top));
+            float sum = o.y * w;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (a.lse && p8 == 0 && r0 + q < rows)
+                a.lse[out_row(r0 + q)] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int k = n * AT + lane / L, r = r0 + k;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < parts; ++p) {
+                    const float4 v = p < 2 ? (p ? x[n][1] : x[n][0]) : load(n, p);
+                    const float f = __shfl_sync(~0u, w, k * 8 + p);
+                    y.x += f * v.x; y.y += f * v.y; y.z += f * v.z; y.w += f * v.w;
+                }
+                const float f = __shfl_sync(~0u, inv, k * 8);
+                if (r < rows)
+                    *reinterpret_cast<uint2*>(a.out + out_row(r) * D + (lane % L) * 4) =
+                        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+            }
+        }
+        return;
+    }
     const int p0 = few ? 0 : warp, dp = few ? 1 : ATT_JOIN_WARPS;  // this warp's parts of a row
     const int r0 = few ? blockIdx.y * ATT_JOIN_WARPS + warp : blockIdx.y;
     const int step = few ? gridDim.y * ATT_JOIN_WARPS : gridDim.y;
@@ -784,8 +849,7 @@ __global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArg
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        const int rr = h.z + r;
-        const int64_t row = (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
+        const int64_t row = out_row(r);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         float acc[V];
 #pragma unroll
