@@ -15,9 +15,12 @@
 // joins in order (so results do not depend on timing).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
-#define ATT_MAX_CTAS 304        // 2 x 152: workspace is sized for this many
+#define ATT_MAX_SMS 152         // the workspace is sized for a grid of this many SMs
+#define ATT_MAX_PER_SM 3        // and so many CTAs on each
 #define ATT_PART_ROWS 256       // rows of partial sums per SM and slot
 #define ATT_JOIN_WARPS 8
 
@@ -174,7 +177,10 @@ __device__ __forceinline__ void att_next(const AttnArgs& a, AttCur& c) {
 // tiles more than it has (what beginning and ending it costs).  Every CTA computes it for
 // itself: one read of the lengths into shared memory, then two block scans, row tiles per
 // request and key tiles per row tile.  `scratch`: att_deal_bytes(B) of shared memory.
-constexpr __host__ __device__ int att_deal_bytes(int B) { return 16 * B + 4 * (B + 1) + 16 + 8 * 32; }
+#define ATT_DEAL_SEQS 1024  // requests whose lengths are kept there; more are read again
+constexpr __host__ __device__ int att_deal_bytes(int B) {
+    return 16 * (B < ATT_DEAL_SEQS ? B : ATT_DEAL_SEQS) + 8 * 32 + 4 * (B + 1);
+}
 
 template <int ROWS, int TK, int NTH, int ALIGN, int OV>
 __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, AttCur& c, int64_t& w0, int64_t& per, int64_t& total,
@@ -197,11 +203,13 @@ __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, At
     }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int4* const seq = reinterpret_cast<int4*>(scratch);
-    int64_t* const red = reinterpret_cast<int64_t*>(scratch + 16 * a.B);
-    int* const base = reinterpret_cast<int*>(scratch + 16 * a.B + 8 * 32);  // first row tile of each request
+    const int kept = min(a.B, ATT_DEAL_SEQS);
+    int64_t* const red = reinterpret_cast<int64_t*>(scratch + 16 * kept);
+    int* const base = reinterpret_cast<int*>(scratch + 16 * kept + 8 * 32);  // first row tile of each request
     __shared__ int s_b, s_rt;
     __shared__ int64_t s_before;
     auto get = [&](int b) {
+        if (b >= kept) return att_seq(a, b);
         const int4 v = seq[b];
         return AttSeq{v.x, v.y, v.z, v.w};
     };
@@ -229,13 +237,13 @@ __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, At
     int64_t mine = 0, entries;
     for (int b = b0; b < b1; ++b) {
         const AttSeq s = att_seq(a, b);
-        seq[b] = make_int4(s.t0, s.n, s.kv, s.pre);
+        if (b < kept) seq[b] = make_int4(s.t0, s.n, s.kv, s.pre);
         mine += ((int64_t)s.n * a.G + ROWS - 1) / ROWS;
     }
     int64_t ex = scan(mine, entries);
     for (int b = b0; b < b1; ++b) {
         base[b] = (int)ex;
-        ex += ((int64_t)seq[b].y * a.G + ROWS - 1) / ROWS;
+        ex += ((int64_t)get(b).n * a.G + ROWS - 1) / ROWS;
     }
     if (tid == 0) base[a.B] = (int)entries;
     __syncthreads();
@@ -298,10 +306,10 @@ template <int D, bool F8, int NTW, int RW, int KW>
 struct AttCfg {
     static constexpr int ES = F8 ? 1 : 2, CH = D * ES / 16;     // 16-byte chunks of a cached row
     static constexpr int NTH = 32 * RW * KW, ROWS = 8 * NTW * RW;
-    static constexpr int PER_SM = NTH > 128 ? 1 : 2;
+    static constexpr int PER_SM = NTH > 128 ? 1 : NTW == 1 ? 3 : 2;
     static constexpr int TK = 32768 / (2 * D * ES) > 128 ? 128 : 32768 / (2 * D * ES);
     static constexpr int STAGE = 2 * TK * D * ES;
-    static constexpr int ST = (PER_SM == 2 ? 98304 : 163840) / STAGE;  // 3 to 10 stages
+    static constexpr int ST = (PER_SM == 3 ? 65536 : PER_SM == 2 ? 98304 : 163840) / STAGE;  // 2 to 10 stages
     static constexpr int KPW = TK / KW;                          // keys of a warp in a tile
     static constexpr int CK = KPW > 32 ? 32 : KPW;               // and in one softmax step
     static constexpr int AROW = D + 4;                           // merge areas, one per row group, padded against bank conflicts
@@ -410,6 +418,8 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
     float acc[NTW][MT][4], m[NTW][2], l[NTW][2], rs[NTW][2], slope[NTW][2];
     int rlo[NTW][2], rhi[NTW][2], rpos[NTW][2];
     int all_lo = 0, all_hi = 0;  // keys that every row of the tile sees
+    const bool extra = a.softcap > 0.f || a.slopes;
+    const float cap_in = 2.f * LOG2E / a.softcap, cap_out = a.softcap * LOG2E;
     float vs = 1.f;
     bool started = false;
 
@@ -535,22 +545,39 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
             uint32_t pb[NTW][SUB][2];
 #pragma unroll
             for (int nt = 0; nt < NTW; ++nt) {
+                if (extra) {
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
+                            float x = s[nt][u][e] * rs[nt][j];
+                            if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
+                                const float y = ex2(x * cap_in);
+                                x = cap_out * (1.f - __fdividef(2.f, 1.f + y));
+                            }
+                            s[nt][u][e] = x - slope[nt][j] * fabsf((float)(rpos[nt][j] - key));
+                        }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[nt][u][e] *= rs[nt][e & 1];
+                }
+                if (masked) {
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
+                            if (key < rlo[nt][j] || key >= rhi[nt][j]) s[nt][u][e] = -INFINITY;
+                        }
+                }
                 float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
-                        float x = s[nt][u][e] * rs[nt][j];
-                        if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
-                            const float y = ex2(x * (2.f * LOG2E) / a.softcap);
-                            x = (a.softcap * LOG2E) * (1.f - __fdividef(2.f, 1.f + y));
-                        }
-                        if (a.slopes) x -= slope[nt][j] * fabsf((float)(rpos[nt][j] - key));
-                        if (masked) x = (key >= rlo[nt][j] && key < rhi[nt][j]) ? x : -INFINITY;
-                        s[nt][u][e] = x;
-                        top[j] = fmaxf(top[j], x);
-                    }
+                    for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[nt][u][e]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -598,6 +625,8 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                 odd |= keep != 0xffffffffu;
                 return x & keep;
             };
+            auto pv = [&](auto masked_tag) {
+                constexpr bool MASKED = decltype(masked_tag)::value;
 #pragma unroll
             for (int u = 0; u < SUB; ++u) {
                 if constexpr (F8) {
@@ -611,7 +640,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                             const uint32_t y0 = e4m3x2_to_f16x2(r[2 * h + 1]), y1 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
                             uint32_t fa[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
                                               __byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
-                            if (masked) {
+                            if constexpr (MASKED) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
                             }
@@ -625,7 +654,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                     for (int k = 0; k < MT; ++k) {
                         uint32_t fa[4];
                         ldsm4t(fa, chunk_addr(stv, kr + u * 16 + (lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
-                        if (masked) {
+                        if constexpr (MASKED) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
                         }
@@ -634,6 +663,9 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                     }
                 }
             }
+            };
+            if (masked) pv(std::true_type{});
+            else pv(std::false_type{});
             if (masked && __any_sync(~0u, odd)) {
 #pragma unroll
                 for (int k = 0; k < MT; ++k)

@@ -39,8 +39,8 @@ AttnWs attn_ws(int D) {
     AttnWs w{};
     size_t o = 0;
     auto put = [&](size_t bytes) { size_t r = o; o += al(bytes); return r; };
-    const size_t slots = (size_t)ATT_MAX_CTAS * ATT_PART_ROWS;  // 2 x CTAs x rows of the widest kernel at 2 CTAs per SM
-    w.hdr = put(ATT_MAX_CTAS * sizeof(int4));
+    const size_t slots = (size_t)2 * ATT_MAX_SMS * ATT_PART_ROWS;  // two per CTA, rows of the widest kernel
+    w.hdr = put(ATT_MAX_SMS * ATT_MAX_PER_SM * sizeof(int4));
     w.ml = put(slots * sizeof(float2));
     w.part = put(slots * D * 4);
     w.total = o;
@@ -147,8 +147,8 @@ cudaError_t launch_attn_join(const AttnArgs& a, int grid, int rows, float lift, 
 template <int D, bool F8, int NTW, int RW, int KW>
 cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
     using C = AttCfg<D, F8, NTW, RW, KW>;
-    static_assert(2 * C::PER_SM * C::ROWS <= 2 * ATT_PART_ROWS, "the workspace holds the partial sums of every CTA");
-    const int grid = std::min(sms * C::PER_SM, ATT_MAX_CTAS * C::PER_SM / 2);
+    static_assert(C::PER_SM * C::ROWS <= ATT_PART_ROWS && C::PER_SM <= ATT_MAX_PER_SM, "the workspace holds every CTA's partial sums");
+    const int grid = std::min(sms, ATT_MAX_SMS) * C::PER_SM;
     k_attn_rows<D, F8, NTW, RW, KW><<<grid, C::NTH, C::SMEM, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, grid, C::ROWS, F8 ? 10.f : 0.f, st) : e;
@@ -156,7 +156,8 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
 
 template <int D, bool F8>
 cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
-    const int grid = std::min(sms, ATT_MAX_CTAS / 2);
+    static_assert(AC_ROWS <= ATT_PART_ROWS, "the workspace holds every CTA's partial sums");
+    const int grid = std::min(sms, ATT_MAX_SMS);
     CUtensorMap tk{}, tv{};
     a.tma = tmap_cache<D, F8>(&tk, a.k, a) && tmap_cache<D, F8>(&tv, a.v, a);
     k_attn_chunk<D, F8><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
