@@ -29,6 +29,16 @@ inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
     return p && q && n && m && a < b + m && b < a + n;
 }
 
+// Four tokens a CTA once that still leaves four CTAs for every SM; below, one token a CTA for the latency.
+template <int D, bool F8>
+void launch_rope(const RopeArgs& a, cudaStream_t st) {
+    const int tok = a.T >= QR_TOKENS * 4 * 148 ? QR_TOKENS : 1, pieces = tok * (a.Hq + 2 * a.Hk) * (D / 16);
+    const int each = tok == 1 ? 1 : QR_UNROLL;  // pieces a thread
+    const int threads = std::min(QR_MAX_THREADS, std::max(64, ((pieces + each - 1) / each + 31) / 32 * 32));
+    if (tok == 1) k_qk_norm_rope<D, F8, 1><<<a.T, threads, 0, st>>>(a);
+    else k_qk_norm_rope<D, F8, QR_TOKENS><<<(a.T + tok - 1) / tok, threads, 0, st>>>(a);
+}
+
 // ---------------------------------------------------------------- attention
 
 struct AttnWs {
@@ -164,14 +174,19 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }
-// Rows of a request that share a cached head, at most: the row tile that wastes least
+// Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 32 the row
+// kernels read the cache once at memory speed and waste no tensor work on absent rows (64 requests of
+// 8 rows at 32K: 184 us, the chunk kernel 383).  Above, the chunk kernel does (64 windows of 5 tokens,
+// 40 rows, at 16K: 312 us, the widest row kernel 520), except that it takes longer to start and end, so a
+// small call (query rows x keys the table can hold below 2^19) stays with the row kernel (5 tokens at
+// 1,000 keys: 15.6 us, the chunk kernel 22.4; 37 tokens at 8,192: 39 us, 33.7).
 template <int D, bool F8>
 cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     const int64_t rows = (int64_t)std::min(a.max_q, a.T) * a.G;
     if (rows <= 8) return launch_attn_rows<D, F8, 1, 1, 4>(a, sms, st);
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
     if (rows <= 32) return launch_attn_rows<D, F8, 2, 2, 4>(a, sms, st);
-    if (rows >= 128) return launch_attn_chunk<D, F8>(a, sms, st);
+    if ((int64_t)a.T * a.G * a.width * a.page_size >= 1 << 19) return launch_attn_chunk<D, F8>(a, sms, st);
     return launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st);
 }
 
@@ -281,9 +296,9 @@ int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride,
     if (!q || !k || !v || !position || !slot || !q_out || (rot_dim > 0 && !inv_freq)) return MOE_ERR_ARG;
     for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)q_out})
         if (!aligned(p, 16)) return MOE_ERR_ARG;
-    for (const void* p : {(const void*)position, (const void*)slot, (const void*)q_norm, (const void*)k_norm,
-                          (const void*)inv_freq})
+    for (const void* p : {(const void*)position, (const void*)slot, (const void*)inv_freq})
         if (!aligned(p, 4)) return MOE_ERR_ARG;
+    if (!aligned(q_norm, 16) || !aligned(k_norm, 16)) return MOE_ERR_ARG;
     // in place (the same rows) is fine: a CTA reads its token's row before it writes it; rows that
     // merely overlap are not
     const size_t qb = ((size_t)(T - 1) * q_stride + qw) * 2, ob = ((size_t)(T - 1) * out_stride + qw) * 2;
@@ -306,13 +321,8 @@ int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride,
     a.page_size = kv->page_size; a.n_slots = (int64_t)kv->n_pages * kv->page_size;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool f8 = kv->kv_type == MOE_KV_E4M3;
-    if (D == 64) {
-        if (f8) k_qk_norm_rope<64, true><<<T, QR_THREADS, 0, st>>>(a);
-        else k_qk_norm_rope<64, false><<<T, QR_THREADS, 0, st>>>(a);
-    } else {
-        if (f8) k_qk_norm_rope<128, true><<<T, QR_THREADS, 0, st>>>(a);
-        else k_qk_norm_rope<128, false><<<T, QR_THREADS, 0, st>>>(a);
-    }
+    if (D == 64) f8 ? launch_rope<64, true>(a, st) : launch_rope<64, false>(a, st);
+    else f8 ? launch_rope<128, true>(a, st) : launch_rope<128, false>(a, st);
     count(1);
     return cuda_rc(cudaGetLastError());
 }

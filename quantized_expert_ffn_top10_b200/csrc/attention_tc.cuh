@@ -36,9 +36,9 @@ template <int D, bool F8>
 struct AcCfg {
     static constexpr int TILE = AC_TK * D * 2;                // one 16-bit operand tile: a half of Q, K or V
     static constexpr int RAW = AC_TK * D;                     // one e4m3 tile as stored
-    static constexpr int NS = D == 64 ? 8 : 4;                // ring of operand tiles: K0 V0 K1 V1 ...
-    static constexpr int NRAW = !F8 ? 0 : D == 64 ? 6 : 2;    // and of e4m3 tiles on their way into it
-    static_assert(NS % 2 == 0 && NRAW % 2 == 0, "a place is always K's or always V's: their warps wait for its phases in order");
+    static constexpr int NS = D == 64 ? 8 : F8 ? 3 : 4;       // ring of operand tiles: K0 V0 K1 V1 ...
+    static constexpr int NRAW = !F8 ? 0 : D == 64 ? 6 : 4;    // and of e4m3 tiles on their way into it
+    static_assert(NRAW % 2 == 0, "a place there is always K's or always V's");
     static constexpr int OFF_RING = 2 * TILE, OFF_RAW = OFF_RING + NS * TILE;
     static constexpr int OFF_ROW = OFF_RAW;                   // gather: row offsets (no e4m3 tile is staged then)
     static constexpr int OFF_ML = OFF_RAW + (F8 ? NRAW * RAW : 2 * AC_TK * 8);
@@ -122,11 +122,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t *const full = bar, *const empty = bar + NS, *const sfull = bar + 2 * NS, *const pfull = sfull + 2,
              *const qready = pfull + 2, *const ofull = qready + 1, *const half_up = ofull + 1, *const half_read = half_up + 1,
-             *const rows_up = half_read + 1, *const cleaned = rows_up + 1, *const raw_full = cleaned + NS,
+             *const rows_up = half_read + 1, *const passed = rows_up + 1, *const cleaned = passed + 2, *const raw_full = cleaned + NS,
              *const raw_empty = raw_full + NRAW;
     uint32_t* const tm = reinterpret_cast<uint32_t*>(raw_empty + NRAW);
     volatile int* const odd = reinterpret_cast<int*>(tm + 2);  // [8]: 1 + the item whose masked tiles held non-finite values
-    static_assert((3 * NS + 9 + 2 * NRAW) * 8 + 8 + 32 <= 448, "barriers");
+    static_assert((3 * NS + 11 + 2 * NRAW) * 8 + 8 + 32 <= 448, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         mbar_init(half_up, 4);
         mbar_init(half_read, 4);
         mbar_init(rows_up, 128);
+        mbar_init(passed, 64);
+        mbar_init(passed + 1, 64);
         for (int i = 0; i < NRAW; ++i) {
             mbar_init(raw_full + i, 1);
             mbar_init(raw_empty + i, 64);
@@ -563,6 +565,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                 }
             };
             slot = rslot = kv;
+            uint32_t seen = 0;  // tiles
             for (; ok && next_piece(); ++item) {
                 int all_lo, all_hi;
                 seen_by_all(all_lo, all_hi);
@@ -571,8 +574,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     const bool masked = kv && (k0 < all_lo || k0 + AC_TK > all_hi);
                     uint8_t* const dst = smem + C::OFF_RING + slot * TILE;
                     if constexpr (F8) {
-                        ok = mbar_wait_fast(raw_full + rslot, rph, 23, rslot) && mbar_wait_fast(empty + slot, ph ^ 1, 24, slot);
+                        ok = mbar_wait_fast(raw_full + rslot, rph, 23, rslot);
+                        // In a ring of odd length a place goes from K to V and back, and its emptiness must be
+                        // waited for in the ring's order (a wait two phases early would pass at once): each
+                        // kind's warps wait until the other's have seen the place before theirs empty.
+                        if constexpr (NS % 2) {
+                            if (kv || seen) ok = ok && mbar_wait_fast(passed + (kv ^ 1), kv ? seen & 1 : (seen & 1) ^ 1, 35, slot);
+                        }
+                        ok = ok && mbar_wait_fast(empty + slot, ph ^ 1, 24, slot);
                         if (!ok) break;
+                        if constexpr (NS % 2) {
+                            mbar_arrive(passed + kv);
+                            ++seen;
+                        }
                         // thread t of 64: piece c of rows t_row, t_row + STEP / 2, ...
                         const uint8_t* const src = smem + C::OFF_RAW + rslot * C::RAW + h_row * D + c * 16;
                         if (masked) {

@@ -149,7 +149,7 @@ struct RopeArgs {
 };
 
 // Eight floats as e4m3, one rounding each, values beyond +-448 at the end of the range.
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&x)[8]) {
+__device__ __forceinline__ uint2 pack_e4m3x8(const float* x) {
     uint32_t r[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -160,118 +160,154 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float (&x)[8]) {
     return make_uint2(r[0], r[1]);
 }
 
-#define QR_THREADS 160
-#define QR_UNROLL 2
+#define QR_UNROLL 3       // 32-byte pieces a thread has in flight
+#define QR_MAX_THREADS 512
+#define QR_TOKENS 4       // tokens of a CTA on chunks
 
-// One CTA per token.  A head is D / 8 lanes of 16 bytes, so a head never
-// crosses a warp: the norm's sum is a shuffle over those lanes and the half
-// layout's partner element sits rot / 16 lanes away.  The token's angles are
-// computed once, by the first rot / 2 threads, while the row's loads are in
-// flight: the turns position * f / 2 pi in fp64, their fraction to sincospi in
-// fp32 (position * f itself passes 2^17, where fp32 would keep 2^-7 rad).
-// Everything between the load and the store is fp32; one rounding to bf16 or
-// e4m3.  Bound by memory on chunks, by one load-to-store latency on windows.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(QR_THREADS) k_qk_norm_rope(RopeArgs a) {
-    constexpr int L = D / 8;  // lanes per head
-    __shared__ float2 cs[D / 2];
-    const int t = blockIdx.x, tid = threadIdx.x;
-    const int32_t slot = a.slot[t];
-    if (slot < 0) return;  // a padding row: nothing of it is read or written
-    if (slot >= a.n_slots) {
-        if (tid == 0) moe_set_status(MOE_ERR_SLOT);
-        return;
+// One CTA per TOK tokens.  A head is D / 16 lanes of two 16-byte chunks, so a head
+// never crosses a warp: the norm's sum is a shuffle over those lanes, and a lane
+// takes the chunks whose elements turn together (8 i and 8 i + rot / 2 in the half
+// layout), so the rotation needs no exchange.  The tokens' angles are computed
+// once, a thread each, while the rows' loads are in flight: the turns
+// position * f / 2 pi in fp64, their fraction to sincospi in fp32 (position * f
+// itself passes 2^17, where fp32 would keep 2^-7 rad).  Everything between the
+// load and the store is fp32; one rounding to bf16 or e4m3.  Bound by memory and
+// instruction issue on chunks, by one load-to-store latency on windows.  Measured
+// at 8,192 tokens of 16 + 2 x 2 heads of 128, 84 MB: TBD us with four tokens a CTA;
+// 44 us with one token a CTA and partners 8 elements at a time by shuffle (shared
+// memory and shuffles at 80% of their rate).
+template <int D, bool E4M3, int TOK>
+__global__ void __launch_bounds__(QR_MAX_THREADS) k_qk_norm_rope(RopeArgs a) {
+    constexpr int L = D / 16;  // lanes per head
+    __shared__ float4 cs[TOK][D / 4];  // cosines and sines, two pairs to an entry, [pairs of a lane / 2][lane]: no bank twice
+    __shared__ int64_t s_place[TOK];   // of the token's slot in the cache, bytes; negative: nothing is written
+    const int t0 = blockIdx.x * TOK, tid = threadIdx.x, nth = blockDim.x, half = a.rot / 2, turning = a.rot / 16;
+    const int nch = (a.Hq + 2 * a.Hk) * L, ntok = min(TOK, a.T - t0), total = ntok * nch;
+    auto token = [&](int i) {  // of piece i
+        int k = 0;
+#pragma unroll
+        for (int j = 1; j < TOK; ++j) k += i >= j * nch;
+        return k;
+    };
+    // element offsets of a lane's two chunks in its head
+    const int l = tid % L;
+    int d0 = l * 16, d1 = d0 + 8;
+    if (!a.interleaved && l < turning) {
+        d0 = l * 8;
+        d1 = d0 + half;
     }
-    const int nch = (a.Hq + 2 * a.Hk) * L;
-    const int64_t place = (int64_t)(slot / a.page_size) * a.page_b + (int64_t)(slot % a.page_size) * a.token_b;
+    const bool turns_here = l < turning;
     bool angles = false;
-    for (int c0 = 0; c0 < nch; c0 += QR_THREADS * QR_UNROLL) {
-        uint4 raw[QR_UNROLL];
+    for (int i0 = 0; i0 < total; i0 += nth * QR_UNROLL) {
+        uint4 raw[QR_UNROLL][2];
 #pragma unroll
         for (int u = 0; u < QR_UNROLL; ++u) {
-            const int c = c0 + u * QR_THREADS + tid, head = c / L, d = (c % L) * 8;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (c < nch) {
+            const int i = i0 + u * nth + tid, k = token(i), head = (i - k * nch) / L;
+            const int64_t t = t0 + k;
+            raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+            if (i < total) {
                 const uint16_t* p = head < a.Hq ? a.q + t * a.q_stride + head * D
                                     : head < a.Hq + a.Hk ? a.k + t * a.k_stride + (head - a.Hq) * D
                                                          : a.v + t * a.v_stride + (head - a.Hq - a.Hk) * D;
-                raw[u] = *reinterpret_cast<const uint4*>(p + d);
+                raw[u][0] = *reinterpret_cast<const uint4*>(p + d0);
+                raw[u][1] = *reinterpret_cast<const uint4*>(p + d1);
             }
         }
         if (!angles) {
-            if (tid < a.rot / 2) {
-                const double turns = (double)a.position[t] * (double)a.inv_freq[tid] * 0.15915494309189535;
+            if (nth - 1 - tid < ntok) {
+                const int32_t slot = __ldg(a.slot + t0 + nth - 1 - tid);
+                int64_t place = -1;  // a padding row
+                if (slot >= a.n_slots) moe_set_status(MOE_ERR_SLOT);
+                else if (slot >= 0) place = (int64_t)(slot / a.page_size) * a.page_b + (int64_t)(slot % a.page_size) * a.token_b;
+                s_place[nth - 1 - tid] = place;
+            }
+            for (int i = tid; i < ntok * half; i += nth) {
+                const int k = TOK == 1 ? 0 : i / half, f = i - k * half, e = f & 7;
+                const double turns = (double)__ldg(a.position + t0 + k) * (double)__ldg(a.inv_freq + f) * 0.15915494309189535;
                 float s, c;
                 sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-                cs[tid] = make_float2(c * a.rot_scale, s * a.rot_scale);
+                reinterpret_cast<float2*>(&cs[k][(e >> 1) * turning + (f >> 3)])[e & 1] = make_float2(c * a.rot_scale, s * a.rot_scale);
             }
             __syncthreads();
             angles = true;
         }
 #pragma unroll
         for (int u = 0; u < QR_UNROLL; ++u) {
-            const int c = c0 + u * QR_THREADS + tid, head = c / L, d = (c % L) * 8;
-            if (c0 + u * QR_THREADS + (tid & ~31) >= nch) continue;  // a warp without work
+            const int i = i0 + u * nth + tid, k = token(i), head = (i - k * nch) / L;
+            if (i0 + u * nth + (tid & ~31) >= total) break;  // a warp without work
+            const int64_t t = t0 + k;
             const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hk;
-            float x[8];
-            const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+            float x[16];
+            const uint32_t w[8] = {raw[u][0].x, raw[u][0].y, raw[u][0].z, raw[u][0].w,
+                                   raw[u][1].x, raw[u][1].y, raw[u][1].z, raw[u][1].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            for (int e = 0; e < 8; ++e) {
+                x[2 * e] = __uint_as_float(w[e] << 16);
+                x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
             }
             const float* nw = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
-            float ss = 0.f;
+            if (a.q_norm || a.k_norm) {
+                float ss = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int m = 1; m < L; m <<= 1) ss += __shfl_xor_sync(~0u, ss, m);
-            if (nw) {
-                const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * __ldg(nw + d + i);
-            }
-            const bool turn = !is_v && d < a.rot;
-            if (a.interleaved) {
-                if (turn) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 r = cs[d / 2 + i];
-                        const float p = x[2 * i], n = x[2 * i + 1];
-                        x[2 * i] = p * r.x - n * r.y;
-                        x[2 * i + 1] = n * r.x + p * r.y;
-                    }
+                for (int e = 0; e < 16; e += 2) {
+                    ss = fmaf(x[e], x[e], ss);
+                    s2 = fmaf(x[e + 1], x[e + 1], s2);
                 }
-            } else if (a.rot) {
-                const int half = a.rot / 2;
-                const bool upper = d >= half;
-                const int src = (tid & 31) + (d < a.rot ? (upper ? -half / 8 : half / 8) : 0);
+                ss += s2;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = __shfl_sync(~0u, x[i], src);
-                    if (turn) {
-                        const float2 r = cs[(upper ? d - half : d) + i];
-                        x[i] = upper ? x[i] * r.x + y * r.y : x[i] * r.x - y * r.y;
+                for (int m = 1; m < L; m <<= 1) ss += __shfl_xor_sync(~0u, ss, m);
+                if (nw) {
+                    const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 n = __ldg(reinterpret_cast<const float4*>(nw + (q < 2 ? d0 : d1)) + (q & 1));
+                        x[4 * q] *= r * n.x;
+                        x[4 * q + 1] *= r * n.y;
+                        x[4 * q + 2] *= r * n.z;
+                        x[4 * q + 3] *= r * n.w;
                     }
                 }
             }
-            if (c >= nch) continue;
+            if (turns_here && !is_v) {
+                auto turn = [](float& p, float& n, float c, float s) {
+                    const float q = p * c - n * s;
+                    n = n * c + p * s;
+                    p = q;
+                };
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // pairs 2e and 2e + 1 of this lane
+                    const float4 r = cs[k][e * turning + l];
+                    if (a.interleaved) {
+                        turn(x[4 * e], x[4 * e + 1], r.x, r.y);
+                        turn(x[4 * e + 2], x[4 * e + 3], r.z, r.w);
+                    } else {
+                        turn(x[2 * e], x[8 + 2 * e], r.x, r.y);
+                        turn(x[2 * e + 1], x[8 + 2 * e + 1], r.z, r.w);
+                    }
+                }
+            }
+            const int64_t place = s_place[k];
+            if (i >= total || place < 0) continue;
             if (is_q || !E4M3) {
-                const uint4 o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                           pack_bf16x2(x[6], x[7]));
-                void* p = is_q ? static_cast<void*>(a.q_out + t * a.out_stride + head * D + d)
-                          : is_v ? a.v_cache + place + (head - a.Hq - a.Hk) * a.head_b + d * 2
-                                 : a.k_cache + place + (head - a.Hq) * a.head_b + d * 2;
-                *static_cast<uint4*>(p) = o;
+                uint16_t* p = is_q ? a.q_out + t * a.out_stride + head * D
+                                   : reinterpret_cast<uint16_t*>(is_v ? a.v_cache + place + (head - a.Hq - a.Hk) * a.head_b
+                                                                      : a.k_cache + place + (head - a.Hq) * a.head_b);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    *reinterpret_cast<uint4*>(p + (c ? d1 : d0)) =
+                        make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                                   pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
             } else {
                 const int h = is_v ? head - a.Hq - a.Hk : head - a.Hq;
                 const float* sc = is_v ? a.v_scale : a.k_scale;
                 if (sc) {
-                    const float s = __ldg(sc + h);
+                    const float s = 1.f / __ldg(sc + h);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], s);
+                    for (int e = 0; e < 16; ++e) x[e] *= s;
                 }
-                *reinterpret_cast<uint2*>((is_v ? a.v_cache : a.k_cache) + place + h * a.head_b + d) = pack_e4m3x8(x);
+                uint8_t* p = (is_v ? a.v_cache : a.k_cache) + place + h * a.head_b;
+                *reinterpret_cast<uint2*>(p + d0) = pack_e4m3x8(x);
+                *reinterpret_cast<uint2*>(p + d1) = pack_e4m3x8(x + 8);
             }
         }
     }
