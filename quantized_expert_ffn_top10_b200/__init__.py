@@ -378,19 +378,20 @@ def _flat(t, n, dtype, where, what, dev):
     """Device pointer of n adjacent elements of this type (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() < n or t.get_device() != dev or not t.is_contiguous():
-        _refuse(where, f"{what} is a contiguous {dtype} tensor of at least {n} elements on the current device")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() >= n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(where, f"{what} is a contiguous {dtype} tensor of at least {n} elements on the current device")
 
 
 def _rows16(t, n, d, where, what, dev):
     """(pointer, elements from row to row) of a bf16 [T, n, d] tensor whose rows are whole."""
-    import torch
-    st = t.stride()
-    if (t.dim() != 3 or t.shape[1] != n or t.shape[2] != d or st[2] != 1 or (n > 1 and st[1] != d)
-            or t.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or t.get_device() != dev):
-        _refuse(where, f"{what} is a bf16 [T, {n}, {d}] tensor with adjacent heads on the current device")
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else max(st[0], n * d)
+    st, shape = t.stride(), t.shape
+    if (len(shape) == 3 and shape[1] == n and shape[2] == d and st[2] == 1 and (n == 1 or st[1] == d)
+            and t.get_device() == dev):
+        import torch
+        if t.dtype is torch.bfloat16 or t.dtype in (torch.int16, torch.uint16):
+            return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], n * d)
+    _refuse(where, f"{what} is a bf16 [T, {n}, {d}] tensor with adjacent heads on the current device")
 
 
 def moe_kv_desc(k_cache, v_cache, n_heads: int, k_scale=None, v_scale=None) -> KvDesc:
@@ -421,12 +422,22 @@ def moe_kv_desc(k_cache, v_cache, n_heads: int, k_scale=None, v_scale=None) -> K
     return d
 
 
-def _on_device(kv, where):
-    import torch
-    dev = torch.cuda.current_device()
+_now = None  # (current device, current stream handle of a device), looked up once: they are half a small call's cost
+
+
+def _here(kv, where, stream):
+    """(current device, stream handle); refuses a cache on another device."""
+    global _now
+    if _now is None:
+        import torch
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _now = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    dev = _now[0]()
     if kv is not None and getattr(kv, "device_index", dev) != dev:
         _refuse(where, "the cache is on another device than the current one")
-    return dev
+    return dev, _now[1](dev) if stream is None else _stream(stream)
 
 
 def moe_kv_map(kv_len, q_len, page_size, free_pages, block_table, kv_len_new, cu_q, position, slot, n_used,
@@ -435,7 +446,7 @@ def moe_kv_map(kv_len, q_len, page_size, free_pages, block_table, kv_len_new, cu
     (all int32 CUDA tensors; position and slot have one entry per row)."""
     import torch
     where, i32 = "moe_kv_map", torch.int32
-    dev = _on_device(None, where)
+    dev, st = _here(None, where, stream)
     B, T = kv_len.numel(), position.numel()
     _need(block_table.dim() == 2 and block_table.shape[0] == B, where, "block_table is [B, width]")
     width = block_table.shape[1]
@@ -445,7 +456,7 @@ def moe_kv_map(kv_len, q_len, page_size, free_pages, block_table, kv_len_new, cu
         _flat(block_table, B * width, i32, where, "block_table", dev), width, T,
         _flat(kv_len_new, B, i32, where, "kv_len_new", dev), _flat(cu_q, B + 1, i32, where, "cu_q", dev),
         _flat(position, T, i32, where, "position", dev), _flat(slot, T, i32, where, "slot", dev),
-        _flat(n_used, 1, i32, where, "n_used", dev), _stream(stream))
+        _flat(n_used, 1, i32, where, "n_used", dev), st)
     return _check(rc, where, raise_on_error)
 
 
@@ -456,7 +467,7 @@ def moe_qk_norm_rope(kv: KvDesc, q, k, v, position, slot, q_out, inv_freq=None, 
     [rot_dim / 2] or None (no rotation); q_norm, k_norm fp32 [dim] or None."""
     import torch
     where, f32, i32 = "moe_qk_norm_rope", torch.float32, torch.int32
-    dev = _on_device(kv, where)
+    dev, st = _here(kv, where, stream)
     T, D = q.shape[0], kv.head_dim
     _need(k.shape[0] == T and v.shape[0] == T and q_out.shape[0] == T, where, "q, k, v and q_out have T rows")
     qp, qs = _rows16(q, kv.n_heads, D, where, "q", dev)
@@ -468,7 +479,7 @@ def moe_qk_norm_rope(kv: KvDesc, q, k, v, position, slot, q_out, inv_freq=None, 
         ctypes.byref(kv), qp, qs, kp, ks, vp, vs, T, _flat(position, T, i32, where, "position", dev),
         _flat(slot, T, i32, where, "slot", dev), _flat(q_norm, D, f32, where, "q_norm", dev),
         _flat(k_norm, D, f32, where, "k_norm", dev), eps, _flat(inv_freq, rot // 2, f32, where, "inv_freq", dev), rot,
-        int(bool(interleaved)), rot_scale, op, os_, _stream(stream))
+        int(bool(interleaved)), rot_scale, op, os_, st)
     return _check(rc, where, raise_on_error)
 
 
@@ -480,7 +491,7 @@ def _attn(fn, where, max_q, kv, q, cu_q, kv_len, block_table, out, ws, scale, so
           stream, raise_on_error):
     import torch
     f32, i32 = torch.float32, torch.int32
-    dev = _on_device(kv, where)
+    dev, st = _here(kv, where, stream)
     T, D, B = q.shape[0], kv.head_dim, kv_len.numel()
     qp, qs = _rows16(q, kv.n_heads, D, where, "q", dev)
     _need(block_table.dim() == 2 and block_table.shape[0] == B, where, "block_table is [B, width]")
@@ -493,7 +504,7 @@ def _attn(fn, where, max_q, kv, q, cu_q, kv_len, block_table, out, ws, scale, so
             _flat(block_table, B * width, i32, where, "block_table", dev), width, *max_q, scale, softcap, window,
             _flat(slopes, kv.n_heads, f32, where, "slopes", dev), _flat(prefix, B, i32, where, "prefix", dev), op,
             _flat(lse, T * kv.n_heads, f32, where, "lse", dev), ws.data_ptr(), ws.numel() * ws.element_size(),
-            _stream(stream))
+            st)
     return _check(rc, where, raise_on_error)
 
 
