@@ -790,129 +790,180 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
     }
 }
 
-// Joins the parts of an item that starts in CTA blockIdx.x and ends in a later
-// one: part 0 in that CTA's second slot, the others in the first slot of the
-// CTAs after it, always in that order.  Rows with up to 8 parts go four to a warp
-// (an item cut once or twice), a row with up to 32 is one warp's, and the 8 warps
-// of a CTA share a row with more (a long cache and few rows).  Bound by latency:
-// the first parts of a row are asked for before their weights.
-template <int D>
-__global__ void __launch_bounds__(32 * ATT_JOIN_WARPS) k_attn_join(const AttnArgs a, int rows_per, float lift) {
-    constexpr int V = D / 32, AHEAD = 8;
+// Joins the parts of an item that starts in CTA c of the grid before and ends in a
+// later one: part 0 in c's second slot, the others in the first slot of the CTAs
+// after it, always in that order.  Units of work: four rows a warp for items of up
+// to 8 parts (cut once or twice), a row a warp up to 32, a row a CTA above (a long
+// cache and few rows).  LIST: every CTA numbers all units from the headers and one
+// wave of CTAs does them; otherwise (few rows an item) CTA (c, y) takes every
+// gridDim.y-th unit of item c, which saves the numbering (1.5 us of 12).  Bound by
+// latency: the first parts of a row are asked for before their weights.
+__device__ __forceinline__ int join_units(int x) {
+    const int parts = x & 0xffff, rows = x >> 16;
+    return parts == 0 ? 0 : parts <= 8 ? (rows + 4 * ATT_JOIN_WARPS - 1) / (4 * ATT_JOIN_WARPS)
+                        : parts <= 32 ? (rows + ATT_JOIN_WARPS - 1) / ATT_JOIN_WARPS : rows;
+}
+
+template <int D, bool LIST>
+__global__ void __launch_bounds__(32 * ATT_JOIN_WARPS, 4) k_attn_join(const AttnArgs a, int n_hdr, int rows_per, float lift) {
+    constexpr int V = D / 32, AHEAD = 8, NTH = 32 * ATT_JOIN_WARPS;
     __shared__ float s_acc[ATT_JOIN_WARPS][D];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 h = a.hdr[c];
-    const int parts = h.x & 0xffff, rows = h.x >> 16;
-    if (parts == 0) return;
-    const bool few = parts <= 32;
-    auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
-    auto out_row = [&](int r) {
-        const int rr = h.z + r;
-        return (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
-    };
-    if (parts <= 8) {
-        constexpr int L = D / 4, AT = 32 / L, N = 4 / AT;  // lanes a row, rows at a time, times
-        const int q = lane >> 3, p8 = lane & 7;            // this lane's row and part of the 4 x 8 weights
-        for (int r0 = (blockIdx.y * ATT_JOIN_WARPS + warp) * 4; r0 < rows; r0 += gridDim.y * ATT_JOIN_WARPS * 4) {
-            const bool live = p8 < parts && r0 + q < rows;
-            const float2 o = live ? a.ml[slot(p8) + r0 + q] : make_float2(-INFINITY, 0.f);
-            float4 x[N][2];
-            auto load = [&](int n, int p) {
-                const int r = r0 + n * AT + lane / L;
-                return p < parts && r < rows ? *reinterpret_cast<const float4*>(a.part + (slot(p) + r) * D + (lane % L) * 4)
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-            };
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                x[n][0] = load(n, 0);
-                x[n][1] = load(n, 1);
-            }
-            float top = o.x;
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const float w = ex2(o.x - (top == -INFINITY ? 0.f : top));
-            float sum = o.y * w;
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            if (a.lse && p8 == 0 && r0 + q < rows)
-                a.lse[out_row(r0 + q)] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int k = n * AT + lane / L, r = r0 + k;
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < parts; ++p) {
-                    const float4 v = p < 2 ? (p ? x[n][1] : x[n][0]) : load(n, p);
-                    const float f = __shfl_sync(~0u, w, k * 8 + p);
-                    y.x += f * v.x; y.y += f * v.y; y.z += f * v.z; y.w += f * v.w;
-                }
-                const float f = __shfl_sync(~0u, inv, k * 8);
-                if (r < rows)
-                    *reinterpret_cast<uint2*>(a.out + out_row(r) * D + (lane % L) * 4) =
-                        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-            }
-        }
-        return;
-    }
-    const int p0 = few ? 0 : warp, dp = few ? 1 : ATT_JOIN_WARPS;  // this warp's parts of a row
-    const int r0 = few ? blockIdx.y * ATT_JOIN_WARPS + warp : blockIdx.y;
-    const int step = few ? gridDim.y * ATT_JOIN_WARPS : gridDim.y;
-    for (int r = r0; r < rows; r += step) {
-        float x[AHEAD][V];
-        auto load = [&](int first) {
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n) {
-                const int p = first + n * dp;
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[n][i] = p < parts ? a.part[(slot(p) + r) * D + i * 32 + lane] : 0.f;
-            }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto unit_of = [&](const int c, const int4 h, const int nth_unit) {
+        const int parts = h.x & 0xffff, rows = h.x >> 16;
+        const bool few = parts <= 32;
+        auto slot = [&](int p) { return (int64_t)(p == 0 ? 2 * c + 1 : 2 * (c + p)) * rows_per; };
+        auto out_row = [&](int r) {
+            const int rr = h.z + r;
+            return (int64_t)(h.y + rr / a.G) * (a.Hk * a.G) + h.w * a.G + rr % a.G;
         };
-        load(p0);
-        float top = -INFINITY;
-        for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        const float ref = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int p = lane; p < parts; p += 32) {
-            const float2 o = a.ml[slot(p) + r];
-            sum += o.y * ex2(o.x - ref);
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        const int64_t row = out_row(r);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        float acc[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
-        for (int first = p0; first < parts; first += AHEAD * dp) {
-            if (first > p0) load(first);
-#pragma unroll
-            for (int n = 0; n < AHEAD; ++n) {
-                const int p = first + n * dp;
-                if (p >= parts) break;
-                const float f = ex2(a.ml[slot(p) + r].x - ref);
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += f * x[n][i];
+        if (parts <= 8) {
+            constexpr int L = D / 4, AT = 32 / L, N = 4 / AT;  // lanes a row, rows at a time, times
+            const int q = lane >> 3, p8 = lane & 7;            // this lane's row and part of the 4 x 8 weights
+            const int r0 = (nth_unit * ATT_JOIN_WARPS + warp) * 4;
+            if (r0 < rows) {
+                const bool live = p8 < parts && r0 + q < rows;
+                const float2 o = live ? a.ml[slot(p8) + r0 + q] : make_float2(-INFINITY, 0.f);
+                float4 x[N][2];
+                auto load = [&](int n, int p) {
+                    const int r = r0 + n * AT + lane / L;
+                    return p < parts && r < rows ? *reinterpret_cast<const float4*>(a.part + (slot(p) + r) * D + (lane % L) * 4)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+    #pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    x[n][0] = load(n, 0);
+                    x[n][1] = load(n, 1);
+                }
+                float top = o.x;
+    #pragma unroll
+                for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const float w = ex2(o.x - (top == -INFINITY ? 0.f : top));
+                float sum = o.y * w;
+    #pragma unroll
+                for (int d = 1; d < 8; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                if (a.lse && p8 == 0 && r0 + q < rows)
+                    a.lse[out_row(r0 + q)] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
+    #pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    const int k = n * AT + lane / L, r = r0 + k;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int p = 0; p < parts; ++p) {
+                        const float4 v = p < 2 ? (p ? x[n][1] : x[n][0]) : load(n, p);
+                        const float f = __shfl_sync(~0u, w, k * 8 + p);
+                        y.x += f * v.x; y.y += f * v.y; y.z += f * v.z; y.w += f * v.w;
+                    }
+                    const float f = __shfl_sync(~0u, inv, k * 8);
+                    if (r < rows)
+                        *reinterpret_cast<uint2*>(a.out + out_row(r) * D + (lane % L) * 4) =
+                            make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+                }
             }
+            return;
         }
-        if (few) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) a.out[row * D + lane + i * 32] = f32_to_bf16_bits(acc[i] * inv);
-        } else {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
-            __syncthreads();
-            if (threadIdx.x < D) {
-                float y = 0.f;
-#pragma unroll
-                for (int w = 0; w < ATT_JOIN_WARPS; ++w) y += s_acc[w][threadIdx.x];
-                a.out[row * D + threadIdx.x] = f32_to_bf16_bits(y * inv);
+        const int p0 = few ? 0 : warp, dp = few ? 1 : ATT_JOIN_WARPS;  // this warp's parts of a row
+        const int r = few ? nth_unit * ATT_JOIN_WARPS + warp : nth_unit;
+        if (r < rows) {  // (the same for the whole CTA where its warps meet below)
+            float x[AHEAD][V];
+            auto load = [&](int first) {
+    #pragma unroll
+                for (int n = 0; n < AHEAD; ++n) {
+                    const int p = first + n * dp;
+    #pragma unroll
+                    for (int i = 0; i < V; ++i) x[n][i] = p < parts ? a.part[(slot(p) + r) * D + i * 32 + lane] : 0.f;
+                }
+            };
+            load(p0);
+            float top = -INFINITY;
+            for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.ml[slot(p) + r].x);
+    #pragma unroll
+            for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const float ref = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            for (int p = lane; p < parts; p += 32) {
+                const float2 o = a.ml[slot(p) + r];
+                sum += o.y * ex2(o.x - ref);
             }
+    #pragma unroll
+            for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            const int64_t row = out_row(r);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float acc[V];
+    #pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = 0.f;
+            for (int first = p0; first < parts; first += AHEAD * dp) {
+                if (first > p0) load(first);
+    #pragma unroll
+                for (int n = 0; n < AHEAD; ++n) {
+                    const int p = first + n * dp;
+                    if (p >= parts) break;
+                    const float f = ex2(a.ml[slot(p) + r].x - ref);
+    #pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] += f * x[n][i];
+                }
+            }
+            if (few) {
+    #pragma unroll
+                for (int i = 0; i < V; ++i) a.out[row * D + lane + i * 32] = f32_to_bf16_bits(acc[i] * inv);
+            } else {
+                __syncthreads();
+    #pragma unroll
+                for (int i = 0; i < V; ++i) s_acc[warp][lane + i * 32] = acc[i];
+                __syncthreads();
+                if (threadIdx.x < D) {
+                    float y = 0.f;
+    #pragma unroll
+                    for (int w = 0; w < ATT_JOIN_WARPS; ++w) y += s_acc[w][threadIdx.x];
+                    a.out[row * D + threadIdx.x] = f32_to_bf16_bits(y * inv);
+                }
+            }
+            if (a.lse && (few ? lane : threadIdx.x) == 0)
+                a.lse[row] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
         }
-        if (a.lse && (few ? lane : threadIdx.x) == 0)
-            a.lse[row] = sum == 0.f ? -INFINITY : (top - lift + log2f(sum)) * 0.6931471805599453f;
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (!LIST) {
+        const int4 h = a.hdr[blockIdx.x];
+        const int n = join_units(h.x);
+        for (int u = blockIdx.y; u < n; u += gridDim.y) unit_of(blockIdx.x, h, u);
+    } else {
+        __shared__ int s_first[2 * NTH], s_sum[ATT_JOIN_WARPS];  // first unit of each header's item
+        __shared__ int4 s_hdr[2 * NTH];
+        static_assert(ATT_MAX_SMS * ATT_MAX_PER_SM <= 2 * NTH, "two headers a thread");
+        int n2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int at = 2 * threadIdx.x + k;
+            const int4 h = at < n_hdr ? a.hdr[at] : make_int4(0, 0, 0, 0);
+            s_hdr[at] = h;
+            n2[k] = join_units(h.x);
+        }
+        int inc = n2[0] + n2[1];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(~0u, inc, d);
+            if (lane >= d) inc += t;
+        }
+        if (lane == 31) s_sum[warp] = inc;
+        __syncthreads();
+        int before = inc - n2[0] - n2[1], units = 0;
+#pragma unroll
+        for (int w = 0; w < ATT_JOIN_WARPS; ++w) {
+            if (w < warp) before += s_sum[w];
+            units += s_sum[w];
+        }
+        s_first[2 * threadIdx.x] = before;
+        s_first[2 * threadIdx.x + 1] = before + n2[0];
+        __syncthreads();
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+            int c = 0;
+            for (int hi = 2 * NTH; hi - c > 1;) {  // the last header whose first unit is at or before this one
+                const int mid = (c + hi) >> 1;
+                if (s_first[mid] <= unit) c = mid;
+                else hi = mid;
+            }
+            unit_of(c, s_hdr[c], unit - s_first[c]);
+        }
     }
 }

@@ -101,7 +101,8 @@ cudaError_t attn_attrs() {
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 1, 4>, AttCfg<D, F8, 2, 1, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 4>, AttCfg<D, F8, 2, 2, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 4, 2>, AttCfg<D, F8, 2, 4, 2>::SMEM);
-    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, false>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, true>, AcCfg<D, F8>::SMEM);
     return e;
 }
 
@@ -141,9 +142,10 @@ bool tmap_cache(CUtensorMap* m, const uint8_t* base, const AttnArgs& a) {
 }
 
 template <int D>
-cudaError_t launch_attn_join(const AttnArgs& a, int grid, int rows, float lift, cudaStream_t st) {
+cudaError_t launch_attn_join(const AttnArgs& a, int sms, int n_hdr, int rows, float lift, cudaStream_t st) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, std::min(rows, 32));
+    const bool list = rows > 16;
+    cfg.gridDim = list ? dim3(4 * sms) : dim3(n_hdr, 8);
     cfg.blockDim = dim3(32 * ATT_JOIN_WARPS);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -151,7 +153,8 @@ cudaError_t launch_attn_join(const AttnArgs& a, int grid, int rows, float lift, 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<D>, a, rows, lift);
+    return list ? cudaLaunchKernelEx(&cfg, k_attn_join<D, true>, a, n_hdr, rows, lift)
+                : cudaLaunchKernelEx(&cfg, k_attn_join<D, false>, a, n_hdr, rows, lift);
 }
 
 template <int D, bool F8, int NTW, int RW, int KW>
@@ -161,7 +164,7 @@ cudaError_t launch_attn_rows(const AttnArgs& a, int sms, cudaStream_t st) {
     const int grid = std::min(sms, ATT_MAX_SMS) * C::PER_SM;
     k_attn_rows<D, F8, NTW, RW, KW><<<grid, C::NTH, C::SMEM, st>>>(a);
     const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? launch_attn_join<D>(a, grid, C::ROWS, F8 ? 10.f : 0.f, st) : e;
+    return e == cudaSuccess ? launch_attn_join<D>(a, sms, grid, C::ROWS, F8 ? 10.f : 0.f, st) : e;
 }
 
 template <int D, bool F8>
@@ -170,9 +173,10 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     const int grid = std::min(sms, ATT_MAX_SMS);
     CUtensorMap tk{}, tv{};
     a.tma = tmap_cache<D, F8>(&tk, a.k, a) && tmap_cache<D, F8>(&tv, a.v, a);
-    k_attn_chunk<D, F8><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
+    if (a.slopes && a.softcap == 0.f) k_attn_chunk<D, F8, true><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
+    else k_attn_chunk<D, F8, false><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
     const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? launch_attn_join<D>(a, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
+    return e == cudaSuccess ? launch_attn_join<D>(a, sms, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }
 // Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 32 the row
 // kernels read the cache once at memory speed and waste no tensor work on absent rows (64 requests of

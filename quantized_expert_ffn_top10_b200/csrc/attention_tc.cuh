@@ -108,7 +108,8 @@ constexpr __host__ __device__ uint32_t ac_idesc(int type, int N, bool b_mn) {
            ((128u >> 4) << 24);
 }
 
-template <int D, bool F8>
+// TILT: slopes without a cap (kept out of the others: its instructions cost them 2%).
+template <int D, bool F8, bool TILT>
 __global__ void __launch_bounds__(AC_THREADS, 1)
     k_attn_chunk(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
     using C = AcCfg<D, F8>;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             const int row0 = duo ? 0 : half * 128, steps = duo ? (cnt + 1 - half) / 2 : cnt;
             const int rr = cur.rt * AC_ROWS + row0 + r, i = rr / a.G, head = cur.h * a.G + rr % a.G;
             const bool mine = row0 + r < rows, busy = __any_sync(~0u, mine);  // a warp without rows only keeps step
-            int lo = 0, hi = 0;
+            int lo = 0, hi = 0x7fffffff;  // (a lane without a row must not make its warp mask)
             if (mine) att_range(a, cur.s, i, lo, hi);
             const int pos = cur.s.kv - cur.s.n + i;
             const float ks = (F8 && a.k_scale) ? __ldg(a.k_scale + cur.h) : 1.f;
@@ -277,9 +278,11 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                 if (busy) {
                     tc_fence_after();
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
-                    const bool masked = __any_sync(~0u, k0 < lo || k0 + AC_TK > hi), edit = masked || !simple;
-                    // scores that are not S times a number, or hidden ones, are put in S's place first
-                    if (edit) {
+                    const bool masked = __any_sync(~0u, k0 < lo || k0 > hi - AC_TK), edit = masked || !simple;
+                    const bool tilted = TILT && !masked && !__any_sync(~0u, mine && k0 + AC_TK - 1 > pos);
+                    // Scores that are not S times a number, or hidden ones, are put in S's place first; but a slope
+                    // alone is linear in the column of a tile behind the row, and is added to the registers below.
+                    if (edit && !tilted) {
                         const int f = masked ? lo - k0 : -1024, e = masked ? hi - k0 : 1024;  // visible columns [f, e)
                         const float p0 = (float)(pos - k0);
 #pragma unroll 1
@@ -310,6 +313,18 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int g = 0; g < 4; ++g) reg_tie32(u + g * 32);
+                    if (tilted) {
+                        const float2 rs2 = make_float2(rs, rs), step = make_float2(2.f * slope, 2.f * slope);
+                        const float at0 = -slope * (float)(pos - k0);
+                        float2 bias = make_float2(at0, at0 + slope);
+#pragma unroll
+                        for (int c = 0; c < 128; c += 2) {
+                            const float2 x = fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), rs2, bias);
+                            u[c] = __float_as_uint(x.x);
+                            u[c + 1] = __float_as_uint(x.y);
+                            bias = add2(bias, step);
+                        }
+                    }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < 128; c += 2)
