@@ -317,6 +317,7 @@ double moe_profile_hit_rate(const uint16_t* pairs, int n_pairs, int L, int E, in
 #define MOE_KV_E4M3 1
 #define MOE_ATTN_MAX_HEADS 512
 #define MOE_ATTN_MAX_B 4096        /* requests of one step                         */
+#define MOE_ATTN_MAX_KV 1073741824 /* keys a request's queries see at most            */
 #define MOE_KV_MAP_MAX_T 1048576   /* rows of one moe_kv_map / moe_qk_norm_rope call */
 typedef struct moe_kv_desc {
     void* k_cache;           /* device */
@@ -380,7 +381,7 @@ int moe_rope_inv_freq(int kind, int rot_dim, double base, double factor, double 
  * Queries and keys of T rows normed per head and turned by their positions,
  * keys and values written into the cache, in one pass.
  *   x <- x / sqrt(mean(x^2) + eps) * norm          (q_norm / k_norm [head_dim]
- *                                                   fp32 (device); NULL: skip)
+ *                                                   fp32 (device, 16-B aligned); NULL: skip)
  *   (a, b) <- (a cos - b sin, b cos + a sin) * rot_scale at the angle
  *   position * inv_freq[i]: a, b are elements i and i + rot_dim / 2 of the head,
  *   or 2i and 2i + 1 when interleaved != 0; elements from rot_dim on stay.
@@ -392,9 +393,9 @@ int moe_rope_inv_freq(int kind, int rot_dim, double base, double factor, double 
  *   [T] int32; inv_freq [rot_dim / 2] fp32 (device); q_out rows out_stride
  *   apart, q itself (same stride) for in place; rot_dim a multiple of 16 up to
  *   head_dim, 0 = no rotation.
- * A row with a negative slot is padding: nothing of it is read or written.  A
- * slot past the cache does the same and latches MOE_ERR_SLOT.  Slots of a call
- * are distinct (of two rows with one slot, parts of either may stay).
+ * A row with a negative slot is padding: nothing is written for it.  A slot past
+ * the cache does the same and latches MOE_ERR_SLOT.  Slots of a call are distinct
+ * (of two rows with one slot, parts of either may stay).
  */
 int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
                      const uint16_t* v, int64_t v_stride, int T, const int32_t* position, const int32_t* slot,
@@ -425,8 +426,8 @@ size_t moe_attn_workspace_bytes(int T, int B, int n_heads, int n_kv_heads, int h
  * rounded to 16 bits (bf16, or fp16 for an E4M3 cache) for the product with v.
  * Values behind kv_len or hidden by the mask are never used, NaN or not.  The
  * lengths are read on the device only, so a captured call replays with new
- * ones.  Rows past max_q of a request and lengths past table_width * page_size
- * are not read; a page id outside the cache reads as zeros and latches
+ * ones.  Rows past max_q of a request and lengths past table_width * page_size or
+ * MOE_ATTN_MAX_KV are not read; a page id outside the cache reads as zeros and latches
  * MOE_ERR_SLOT.  Results do not depend on timing.
  */
 int moe_attn_decode(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, int T, const int32_t* cu_q,

@@ -53,7 +53,7 @@ MOE_SLOT_REMOTE = -2
 MOE_DBG_SPIN_LIMIT, MOE_DBG_BARRIER_EXTRA = 1, 2
 MOE_WS_FAST_LOGITS, MOE_WS_PAIR_OUT, MOE_WS_SLOW_COUNT = 1, 2, 3
 MOE_KV_BF16, MOE_KV_E4M3 = 0, 1
-MOE_ATTN_MAX_HEADS, MOE_ATTN_MAX_B, MOE_KV_MAP_MAX_T = 512, 4096, 1048576
+MOE_ATTN_MAX_HEADS, MOE_ATTN_MAX_B, MOE_ATTN_MAX_KV, MOE_KV_MAP_MAX_T = 512, 4096, 1 << 30, 1048576
 MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_PARTS = 0, 1, 2, 3
 
 

@@ -119,7 +119,7 @@ __device__ __forceinline__ AttSeq att_seq(const AttnArgs& a, int b) {
     AttSeq s;
     s.t0 = min(max(a.cu[b], 0), a.T);
     s.n = min(min(max(a.cu[b + 1], s.t0), a.T) - s.t0, a.max_q);
-    s.kv = min(max(a.kv_len[b], 0), (int)min((int64_t)a.width * a.page_size, (int64_t)0x7fffffff));
+    s.kv = min(max(a.kv_len[b], 0), (int)min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV));
     s.pre = a.prefix ? min(max(a.prefix[b], 0), s.kv) : 0;
     return s;
 }

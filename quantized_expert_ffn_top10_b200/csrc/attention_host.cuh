@@ -190,7 +190,8 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     if (rows <= 8) return launch_attn_rows<D, F8, 1, 1, 4>(a, sms, st);
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
     if (rows <= 32) return launch_attn_rows<D, F8, 2, 2, 4>(a, sms, st);
-    if ((int64_t)a.T * a.G * a.width * a.page_size >= 1 << 19) return launch_attn_chunk<D, F8>(a, sms, st);
+    const int64_t keys = std::min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV);
+    if ((int64_t)a.T * a.G * keys >= 1 << 19) return launch_attn_chunk<D, F8>(a, sms, st);
     return launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st);
 }
 

@@ -111,6 +111,7 @@ def test_rope_refusals(lib):
     for name in ("q", "k", "v", "pos", "slot", "inv", "out"):
         assert r(**{name: None}) == M.MOE_ERR_ARG, name
     assert r(k=3 * FAKE + 4104) == M.MOE_ERR_ARG and r(pos=4 * FAKE + 2) == M.MOE_ERR_ARG
+    assert r(qn=FAKE + 4) == M.MOE_ERR_ARG and r(kn=FAKE + 8) == M.MOE_ERR_ARG
     assert r(out=3 * FAKE + 16) == M.MOE_ERR_ARG            # q_out overlaps q without being q
     assert r(out=3 * FAKE, os_=2048) == M.MOE_ERR_ARG       # q itself, but rows at another stride
     assert r(T=0) == M.MOE_OK

@@ -90,6 +90,11 @@ SHAPES = [
     dict(q_len=[1] * 40, kv_len=list(range(1, 400, 10)), Hq=8, Hk=4, D=64, page=16, head_major=True),
     dict(q_len=[2] * 7, kv_len=[2000, 3, 17, 129, 500, 256, 2], Hq=20, Hk=4, page=32, one_buffer=True),
     dict(q_len=[5], kv_len=[6000], Hq=16, Hk=2, page=64),          # one request over every CTA
+    # wide windows over long caches: the chunk kernel, its two key streams, items cut over many CTAs
+    dict(q_len=[5], kv_len=[20011], Hq=16, Hk=2, page=64),
+    dict(q_len=[8], kv_len=[9000], Hq=10, Hk=1, page=24),
+    dict(q_len=[5, 4, 0, 5, 1, 5], kv_len=[3000, 129, 7, 2048, 5000, 4], Hq=20, Hk=2, D=64, page=256, head_major=True),
+    dict(q_len=[8] * 12, kv_len=[128 * i + i for i in range(1, 13)], Hq=32, Hk=2, page=8, one_buffer=True),
 ]
 EXTRAS = [
     dict(), dict(f8=True), dict(f8=True, scales=False, softcap=20.0), dict(softcap=15.0, window=37), dict(slopes=True),
@@ -146,8 +151,8 @@ def test_hidden_values_never_count(cuda_ok, which, f8):
     reach it (they may reach the rows that see them): the last cached tokens of
     a causal window, and the first ones of a sliding window."""
     import torch
-    n, kv = (5, 150) if which == "decode" else (70, 150)
-    for window, at in ((0, kv - 1), (0, kv - 2), (20, 3 if which == "decode" else 85)):
+    n, kv = (5, 150) if which == "decode" else (70, 2500)
+    for window, at in ((0, kv - 1), (0, kv - 2), (20, 3 if which == "decode" else kv - 65)):
         c = Case([n], [kv], Hq=6, Hk=2, page=16, f8=f8, window=window, seed=11)
         page, off = int(c.cache.table[0, at // 16]), at % 16
         for x, vals in ((c.cache.k, (np.nan,)), (c.cache.v, (np.nan, np.nan) if f8 else (np.inf, np.nan))):
@@ -219,6 +224,54 @@ def test_bad_pages_are_reported_and_read_as_zeros(cuda_ok, which):
     for x in (c.keys, c.values):
         x[0][16:48] = 0.0
     c.check()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_a_window_over_a_128k_cache(cuda_ok, f8):
+    """Every CTA holds a piece of one of two heads, some of both."""
+    c = Case([5], [131072], Hq=16, Hk=2, page=64, f8=f8, seed=23)
+    c.run("decode")
+    c.check()
+
+
+def test_many_requests(cuda_ok):
+    """More requests than a CTA keeps the lengths of."""
+    rng = np.random.default_rng(24)
+    n = 1300
+    c = Case([1] * n, [int(x) for x in rng.integers(0, 70, n)], Hq=2, Hk=1, D=64, page=16, seed=24)
+    c.run("decode")
+    c.check()
+    q = [int(x) for x in rng.integers(0, 3, n)]
+    c = Case(q, [x + 5 for x in q], Hq=3, Hk=1, D=64, page=16, seed=25)
+    c.run("prefill")
+    c.check()
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_offsets_outside_the_step_touch_nothing(cuda_ok, which):
+    """Offsets past the rows, falling ones, and requests without rows."""
+    import torch
+    c = Case([3, 2], [40, 9], Hq=4, Hk=2, page=16, seed=26)
+    for cu in ([0, 0, 0], [5, 5, 5], [7, 900, 3], [-4, -2, -1]):
+        c.cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        c.out.fill_(7.0)
+        c.run(which, max_q=8)
+        torch.cuda.synchronize()
+        assert M.moe_last_device_error() == 0
+        assert bool((c.out == 7.0).all()), cu
+    c.cu = torch.tensor([0, 3, 1 << 30], dtype=torch.int32, device="cuda")  # cut to the rows there are
+    c.out.fill_(7.0)
+    c.run(which, max_q=8)
+    c.check()
+
+
+def test_windows_wider_than_promised_are_cut(cuda_ok):
+    """Rows past max_q of a request are left as they were."""
+    import torch
+    c = Case([3], [40], Hq=4, Hk=2, page=16, seed=27)
+    c.run("decode", max_q=2)
+    torch.cuda.synchronize()
+    assert bool((c.out[2] == 7.0).all()) and not bool((c.out[0] == 7.0).all())
 
 
 def test_lengths_past_the_table_are_cut(cuda_ok):
