@@ -307,9 +307,10 @@ struct AttCfg {
     static constexpr int ES = F8 ? 1 : 2, CH = D * ES / 16;     // 16-byte chunks of a cached row
     static constexpr int NTH = 32 * RW * KW, ROWS = 8 * NTW * RW;
     static constexpr int PER_SM = NTH > 128 ? 1 : NTW == 1 && !(F8 && D == 128) ? 3 : 2;
-    static constexpr int TK = 32768 / (2 * D * ES) > 128 ? 128 : 32768 / (2 * D * ES);
+    static constexpr int WANT = RW == 2 ? 16384 : 32768;         // bytes of a stage
+    static constexpr int TK = WANT / (2 * D * ES) > 128 ? 128 : WANT / (2 * D * ES);
     static constexpr int STAGE = 2 * TK * D * ES;
-    static constexpr int ST = (PER_SM == 3 ? 65536 : PER_SM == 2 ? 98304 : 163840) / STAGE;  // 2 to 10 stages
+    static constexpr int ST = (PER_SM == 3 ? 65536 : RW == 2 ? 81920 : PER_SM == 2 ? 98304 : 163840) / STAGE;  // 2 to 10 stages
     static constexpr int KPW = TK / KW;                          // keys of a warp in a tile
     static constexpr int CK = F8 || KPW < 32 ? 16 : 32;           // and in one softmax step
     static constexpr int AROW = D + 4;                           // merge areas, one per row group, padded against bank conflicts

@@ -99,7 +99,7 @@ template <int D, bool F8>
 cudaError_t attn_attrs() {
     cudaError_t e = set_smem(k_attn_rows<D, F8, 1, 1, 4>, AttCfg<D, F8, 1, 1, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 1, 4>, AttCfg<D, F8, 2, 1, 4>::SMEM);
-    if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 4>, AttCfg<D, F8, 2, 2, 4>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 2>, AttCfg<D, F8, 2, 2, 2>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 4, 2>, AttCfg<D, F8, 2, 4, 2>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, false>, AcCfg<D, F8>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, true>, AcCfg<D, F8>::SMEM);
@@ -178,21 +178,23 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, sms, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }
-// Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 32 the row
-// kernels read the cache once at memory speed and waste no tensor work on absent rows (64 requests of
-// 8 rows at 32K: 184 us, the chunk kernel 383).  Above, the chunk kernel does (64 windows of 5 tokens,
-// 40 rows, at 16K: 312 us, the widest row kernel 520), except that it takes longer to start and end, so a
-// small call (query rows x keys the table can hold below 2^19) stays with the row kernel (5 tokens at
-// 1,000 keys: 15.6 us, the chunk kernel 22.4; 37 tokens at 8,192: 39 us, 33.7).
+// Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 16 the row
+// kernels read the cache at memory speed and waste no tensor work on absent rows (64 requests of 8 rows
+// at 32K: 185 us, the chunk kernel 383; of 16 rows at 16K: 242 us, 278).  Above, the chunk kernel does
+// (48 windows of 24 rows at 20K: 144 us, row kernel 196; 64 of 40 rows at 16K: 300 us, 520), except
+// that it takes longer to start and end, so a small call (query rows x keys the table can hold below
+// 2^19) stays with the row kernels (5 tokens of 8 heads a cached one at 1,000 keys: 15.4 us, the chunk
+// kernel 22; 37 tokens at 8,192: 39 us, 34), and that capped scores cost it more (24 windows of 25 rows
+// in a 4K sliding window: 89 us, 97).
 template <int D, bool F8>
 cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     const int64_t rows = (int64_t)std::min(a.max_q, a.T) * a.G;
     if (rows <= 8) return launch_attn_rows<D, F8, 1, 1, 4>(a, sms, st);
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
-    if (rows <= 32) return launch_attn_rows<D, F8, 2, 2, 4>(a, sms, st);
     const int64_t keys = std::min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV);
-    if ((int64_t)a.T * a.G * keys >= 1 << 19) return launch_attn_chunk<D, F8>(a, sms, st);
-    return launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st);
+    const bool small = (int64_t)a.T * a.G * keys < 1 << 19;
+    if (rows <= 32 && (small || a.softcap > 0.f)) return launch_attn_rows<D, F8, 2, 2, 2>(a, sms, st);
+    return small ? launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st) : launch_attn_chunk<D, F8>(a, sms, st);
 }
 
 int run_attn(const AttnCall& c) {
