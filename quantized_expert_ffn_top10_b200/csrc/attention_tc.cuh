@@ -30,7 +30,10 @@
 #define AC_THREADS 512
 #define AC_ROWS 256
 #define AC_TK 128
-#define AC_OV 4  // an item's beginning and end, in key tiles: measured TBD
+// An item's beginning and end, in key tiles, for the deal.  A chunk's first rows are items of one tile or
+// two, and the CTAs that get them end last unless this is counted: 8,192 tokens from the first, bf16 / e4m3:
+// 495 / 692 us at 1, 412 / 582 at 2, 303 / 424 at 4, 292 / 342 at 6, 298 / 340 at 8, 303 / 346 at 10.
+#define AC_OV 6
 
 template <int D, bool F8>
 struct AcCfg {
