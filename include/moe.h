@@ -413,7 +413,7 @@ size_t moe_attn_workspace_bytes(int T, int B, int n_heads, int n_kv_heads, int h
  *   Row t = cu_q[b] + i sits at position pos = kv_len[b] - (cu_q[b + 1] -
  *   cu_q[b]) + i and sees keys j with j <= pos, or j < prefix[b] (a part of the
  *   prompt whose tokens see one another), and j > pos - window when window > 0.
- *   s_j = scale * q . k_j; softcap > 0: softcap * tanh(s_j / softcap); slopes:
+ *   s_j = scale * q . k_j; softcap (0, or 1e-30 at least): softcap * tanh(s_j / softcap); slopes:
  *   s_j - slopes[head] * |pos - j|.
  *   out = sum_j softmax(s)_j v_j, rounded to bf16; lse = log sum_j exp(s_j).
  *   A row that sees no key gives out 0 and lse -inf.

@@ -79,7 +79,8 @@ int check_attn(const AttnCall& c, int max_T) {
     int rc = check_kv_desc(c.d);
     if (rc) return rc;
     if (c.T < 0 || c.T > max_T || c.B < 0 || c.B > MOE_ATTN_MAX_B || c.width < 1 || c.max_q < 1) return MOE_ERR_RANGE;
-    if (c.window < 0 || !(c.softcap >= 0.f) || !isfinite(c.softcap) || !isfinite(c.scale)) return MOE_ERR_RANGE;
+    if (c.window < 0 || !isfinite(c.softcap) || !isfinite(c.scale)) return MOE_ERR_RANGE;
+    if (c.softcap != 0.f && !(c.softcap >= 1e-30f)) return MOE_ERR_RANGE;  // (its reciprocal is used)
     const int64_t row = (int64_t)c.d->n_heads * c.d->head_dim;
     if (c.q_stride < row || c.q_stride % 8) return MOE_ERR_SHAPE;
     if (c.T == 0 || c.B == 0) return MOE_OK;  // nothing to do: the buffers may be null

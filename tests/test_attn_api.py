@@ -74,6 +74,7 @@ def test_attention_refusals(lib, which):
     assert a(window=-1) == M.MOE_ERR_RANGE
     assert a(softcap=-1.0) == M.MOE_ERR_RANGE and a(softcap=math.nan) == M.MOE_ERR_RANGE
     assert a(softcap=math.inf) == M.MOE_ERR_RANGE and a(scale=math.nan) == M.MOE_ERR_RANGE
+    assert a(softcap=1e-38) == M.MOE_ERR_RANGE
     assert a(q_stride=2040) == M.MOE_ERR_SHAPE and a(q_stride=2052) == M.MOE_ERR_SHAPE
     for name in ("q", "cu", "kv", "table", "out", "ws"):
         assert a(**{name: None}) == M.MOE_ERR_ARG, name

@@ -380,3 +380,31 @@ def test_wrong_tensors_are_refused(cuda_ok):
         M.moe_kv_desc(c.cache.k, c.cache.v[:, :8], 4)
     torch.cuda.synchronize()
     assert bool((c.out == 7.0).all())
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_caches_as_plain_bits(cuda_ok, f8):
+    """int16 stands for bf16 and uint8 for e4m3, for queries and outputs too."""
+    import torch
+    c = Case([2], [50], Hq=4, Hk=2, page=16, f8=f8, seed=28)
+    bits = torch.uint8 if f8 else torch.int16
+    c.desc = M.moe_kv_desc(c.cache.k.view(bits), c.cache.v.view(bits), 4, c.cache.k_scale, c.cache.v_scale)
+    out, c.t_q = c.out, c.t_q.view(torch.int16)
+    c.out = out.view(torch.int16)
+    c.run("decode")
+    c.out = out
+    c.check()
+
+
+def test_empty_batches(cuda_ok):
+    """A step whose requests all sit out, and one without requests, change nothing."""
+    import torch
+    c = Case([2, 1], [50, 9], Hq=4, Hk=2, page=16, seed=29)
+    c.cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for which in ("decode", "prefill"):
+        c.run(which, max_q=4)
+    c.kv, c.cu = c.kv[:0], c.cu[:1]
+    for which in ("decode", "prefill"):
+        c.run(which, max_q=4, table=c.cache.table_dev[:0])
+    torch.cuda.synchronize()
+    assert M.moe_last_device_error() == 0 and bool((c.out == 7.0).all()) and bool((c.lse == 7.0).all())

@@ -170,7 +170,9 @@ def _rope_case(T, Hq, Hk, D, rot, interleaved, norm, f8, page=16, head_major=Fal
 
 @pytest.mark.parametrize("T,Hq,Hk,D,rot,page", [
     (1, 16, 2, 128, 128, 16), (5, 16, 2, 128, 128, 64), (8, 1, 1, 64, 64, 1), (7, 3, 1, 64, 16, 48), (33, 5, 5, 128, 32, 8),
-    (130, 32, 8, 64, 48, 16), (3, 20, 4, 128, 0, 16), (64, 40, 8, 128, 96, 32), (1025, 4, 2, 64, 64, 16)])
+    (130, 32, 8, 64, 48, 16), (3, 20, 4, 128, 0, 16), (64, 40, 8, 128, 96, 32), (1025, 4, 2, 64, 64, 16),
+    # several tokens to a CTA: a ragged last one, one head a token, more heads than a CTA has threads for at once
+    (2371, 5, 1, 64, 32, 16), (2400, 1, 1, 128, 128, 64), (2369, 64, 8, 128, 112, 32)])
 @pytest.mark.parametrize("f8", [False, True])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_norm_and_rotation(cuda_ok, T, Hq, Hk, D, rot, page, f8, interleaved):
