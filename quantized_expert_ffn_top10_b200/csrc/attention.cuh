@@ -312,7 +312,7 @@ struct AttCfg {
     static constexpr int STAGE = 2 * TK * D * ES;
     static constexpr int ST = (PER_SM == 3 ? 65536 : RW == 2 ? 81920 : PER_SM == 2 ? 98304 : 163840) / STAGE;  // 2 to 10 stages
     static constexpr int KPW = TK / KW;                          // keys of a warp in a tile
-    static constexpr int CK = F8 || KPW < 32 ? 16 : 32;           // and in one softmax step
+    static constexpr int CK = F8 || KPW < 32 ? 16 : 32;           // and in one softmax step (e4m3: 32 spills)
     static constexpr int AROW = D + 4;                           // merge areas, one per row group, padded against bank conflicts
     static constexpr int AREA_B = 8 * NTW * AROW * 4;
     static constexpr int OFF_AREA = ST * STAGE, OFF_ML = OFF_AREA + RW * AREA_B;
@@ -629,41 +629,41 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
             auto pv = [&](auto masked_tag) {
                 constexpr bool MASKED = decltype(masked_tag)::value;
 #pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                if constexpr (F8) {
+                for (int u = 0; u < SUB; ++u) {
+                    if constexpr (F8) {
 #pragma unroll
-                    for (int k2 = 0; k2 < MT / 2; ++k2) {
-                        uint32_t r[4];
-                        ldsm4t(r, chunk_addr(stv, kr + u * 16 + (lane & 15), k2 * 2 + (lane >> 4)));
+                        for (int k2 = 0; k2 < MT / 2; ++k2) {
+                            uint32_t r[4];
+                            ldsm4t(r, chunk_addr(stv, kr + u * 16 + (lane & 15), k2 * 2 + (lane >> 4)));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t x0 = e4m3x2_to_f16x2(r[2 * h]), x1 = e4m3x2_to_f16x2(r[2 * h] >> 16);
-                            const uint32_t y0 = e4m3x2_to_f16x2(r[2 * h + 1]), y1 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
-                            uint32_t fa[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
-                                              __byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t x0 = e4m3x2_to_f16x2(r[2 * h]), x1 = e4m3x2_to_f16x2(r[2 * h] >> 16);
+                                const uint32_t y0 = e4m3x2_to_f16x2(r[2 * h + 1]), y1 = e4m3x2_to_f16x2(r[2 * h + 1] >> 16);
+                                uint32_t fa[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                                                  __byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632)};
+                                if constexpr (MASKED) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NTW; ++nt)
+                                    mma16816<true>(acc[nt][2 * k2 + h], fa, pb[nt][u][0], pb[nt][u][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            uint32_t fa[4];
+                            ldsm4t(fa, chunk_addr(stv, kr + u * 16 + (lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
                             if constexpr (MASKED) {
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NTW; ++nt)
-                                mma16816<true>(acc[nt][2 * k2 + h], fa, pb[nt][u][0], pb[nt][u][1]);
+                            for (int nt = 0; nt < NTW; ++nt) mma16816<false>(acc[nt][k], fa, pb[nt][u][0], pb[nt][u][1]);
                         }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < MT; ++k) {
-                        uint32_t fa[4];
-                        ldsm4t(fa, chunk_addr(stv, kr + u * 16 + (lane & 7) + (lane >> 4) * 8, k * 2 + ((lane >> 3) & 1)));
-                        if constexpr (MASKED) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) fa[e] = clean(fa[e]);
-                        }
-#pragma unroll
-                        for (int nt = 0; nt < NTW; ++nt) mma16816<false>(acc[nt][k], fa, pb[nt][u][0], pb[nt][u][1]);
                     }
                 }
-            }
             };
             if (masked) pv(std::true_type{});
             else pv(std::false_type{});
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
 // to 8 parts (cut once or twice), a row a warp up to 32, a row a CTA above (a long
 // cache and few rows).  LIST: every CTA numbers all units from the headers and one
 // wave of CTAs does them; otherwise (few rows an item) CTA (c, y) takes every
-// gridDim.y-th unit of item c, which saves the numbering (1.5 us of 12).  Bound by
+// gridDim.y-th unit of item c, which saves the numbering (1 us of 12).  Bound by
 // latency: the first parts of a row are asked for before their weights.
 __device__ __forceinline__ int join_units(int x) {
     const int parts = x & 0xffff, rows = x >> 16;

@@ -41,7 +41,6 @@ struct AcCfg {
     static constexpr int RAW = AC_TK * D;                     // one e4m3 tile as stored
     static constexpr int NS = D == 64 ? 8 : F8 ? 3 : 4;       // ring of operand tiles: K0 V0 K1 V1 ...
     static constexpr int NRAW = !F8 ? 0 : D == 64 ? 6 : 4;    // and of e4m3 tiles on their way into it
-    static_assert(NRAW % 2 == 0, "a place there is always K's or always V's");
     static constexpr int OFF_RING = 2 * TILE, OFF_RAW = OFF_RING + NS * TILE;
     static constexpr int OFF_ROW = OFF_RAW;                   // gather: row offsets (no e4m3 tile is staged then)
     static constexpr int OFF_ML = OFF_RAW + (F8 ? NRAW * RAW : 2 * AC_TK * 8);
@@ -126,17 +125,17 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
     uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t *const full = bar, *const empty = bar + NS, *const sfull = bar + 2 * NS, *const pfull = sfull + 2,
              *const qready = pfull + 2, *const ofull = qready + 1, *const half_up = ofull + 1, *const half_read = half_up + 1,
-             *const rows_up = half_read + 1, *const passed = rows_up + 1, *const cleaned = passed + 2, *const raw_full = cleaned + NS,
+             *const rows_up = half_read + 1, *const cleaned = rows_up + 1, *const raw_full = cleaned + NS,
              *const raw_empty = raw_full + NRAW;
     uint32_t* const tm = reinterpret_cast<uint32_t*>(raw_empty + NRAW);
     volatile int* const odd = reinterpret_cast<int*>(tm + 2);  // [8]: 1 + the item whose masked tiles held non-finite values
-    static_assert((3 * NS + 11 + 2 * NRAW) * 8 + 8 + 32 <= 448, "barriers");
+    static_assert((3 * NS + 9 + 2 * NRAW) * 8 + 8 + 32 <= 448, "barriers");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(full + i, !a.tma ? 128 : F8 ? 64 : 1);
+            mbar_init(full + i, F8 || !a.tma ? 128 : 1);
             mbar_init(empty + i, 1);
             mbar_init(cleaned + i, 128);
         }
@@ -149,11 +148,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         mbar_init(half_up, 4);
         mbar_init(half_read, 4);
         mbar_init(rows_up, 128);
-        mbar_init(passed, 64);
-        mbar_init(passed + 1, 64);
         for (int i = 0; i < NRAW; ++i) {
             mbar_init(raw_full + i, 1);
-            mbar_init(raw_empty + i, 64);
+            mbar_init(raw_empty + i, 128);
         }
         fence_mbar_init();
         for (int i = 0; i < 8; ++i) odd[i] = 0;
@@ -539,10 +536,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         };
         // 16 e4m3 values into their two pieces of this thread's first row of a tile; its rows are STEP (a
         // multiple of 8) apart, so the others' places differ by a constant
-        static_assert(!F8 || STEP % 16 == 0, "the swizzle repeats every 8 rows");
-        const int h_row = F8 && a.tma ? (t & 63) / CHG : t_row;  // (64 threads to a tile, or 128)
+        static_assert(!F8 || STEP % 8 == 0, "the swizzle repeats every 8 rows");
         const bool turn = D == 128 && (c & 4);  // the second block's lanes start with the other piece: no bank twice
-        const int at0 = place(h_row, 2 * c + turn), at1 = place(h_row, 2 * c + 1 - turn);
+        const int at0 = place(t_row, 2 * c + turn), at1 = place(t_row, 2 * c + 1 - turn);
         auto widen = [&](uint4 w, uint8_t* dst, bool clean, int item) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
             uint32_t y[8];
@@ -573,63 +569,47 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         auto step = [&] { if (++slot == NS) { slot = 0; ph ^= 1; } };
         bool ok = true;
         if (a.tma) {
-            // e4m3: warps 8 and 9 widen the K tiles, 10 and 11 the V tiles; bf16: all four watch the V tiles
-            const int kv = F8 ? (warp - 8) >> 1 : 1;
-            auto step2 = [&](int& s, uint32_t& p, int n) {
-                s += 2;
-                if (s >= n) {
-                    s -= n;
-                    p ^= 1;
-                }
-            };
-            slot = rslot = kv;
-            uint32_t seen = 0;  // tiles
+            // e4m3: the four warps widen every tile together, in the ring's order; bf16: they watch the V tiles
             for (; ok && next_piece(); ++item) {
                 int all_lo, all_hi;
                 seen_by_all(all_lo, all_hi);
-                for (int j = 0; j < cnt; ++j) {
+                for (int j = 0; j < cnt && ok; ++j) {
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
-                    const bool masked = kv && (k0 < all_lo || k0 + AC_TK > all_hi);
-                    uint8_t* const dst = smem + C::OFF_RING + slot * TILE;
-                    if constexpr (F8) {
-                        ok = mbar_wait_fast(raw_full + rslot, rph, 23, rslot);
-                        // In a ring of odd length a place goes from K to V and back, and its emptiness must be
-                        // waited for in the ring's order (a wait two phases early would pass at once): each
-                        // kind's warps wait until the other's have seen the place before theirs empty.
-                        if constexpr (NS % 2) {
-                            if (kv || seen) ok = ok && mbar_wait_fast(passed + (kv ^ 1), kv ? seen & 1 : (seen & 1) ^ 1, 35, slot);
-                        }
-                        ok = ok && mbar_wait_fast(empty + slot, ph ^ 1, 24, slot);
-                        if (!ok) break;
-                        if constexpr (NS % 2) {
-                            mbar_arrive(passed + kv);
-                            ++seen;
-                        }
-                        // thread t of 64: piece c of rows t_row, t_row + STEP / 2, ...
-                        const uint8_t* const src = smem + C::OFF_RAW + rslot * C::RAW + h_row * D + c * 16;
-                        if (masked) {
+                    const bool some_hidden = k0 < all_lo || k0 + AC_TK > all_hi;
 #pragma unroll 1
-                            for (int n = 0; n < 2 * AC_TK / STEP; ++n)
-                                widen(*reinterpret_cast<const uint4*>(src + n * (STEP / 2) * D), dst + n * (STEP / 2) * 128, true, item);
-                        } else {
+                    for (int kv = 0; kv < 2; ++kv, step()) {
+                        const bool masked = kv && some_hidden;
+                        uint8_t* const dst = smem + C::OFF_RING + slot * TILE;
+                        if constexpr (F8) {
+                            ok = mbar_wait_fast(raw_full + rslot, rph, 23, rslot) && mbar_wait_fast(empty + slot, ph ^ 1, 24, slot);
+                            if (!ok) break;
+                            const uint8_t* const src = smem + C::OFF_RAW + rslot * C::RAW + t_row * D + c * 16;
+                            if (masked) {
+#pragma unroll 1
+                                for (int n = 0; n < AC_TK / STEP; ++n)
+                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, true, item);
+                            } else {
 #pragma unroll 4
-                            for (int n = 0; n < 2 * AC_TK / STEP; ++n)
-                                widen(*reinterpret_cast<const uint4*>(src + n * (STEP / 2) * D), dst + n * (STEP / 2) * 128, false, item);
-                        }
-                        mbar_arrive(raw_empty + rslot);
-                        fence_proxy_async_smem();
-                        mbar_arrive(full + slot);
-                        step2(rslot, rph, NRAW);
-                    } else {  // every V tile passes through here, so that the phases cannot run apart
-                        ok = mbar_wait_fast(full + slot, ph, 23, slot);
-                        if (!ok) break;
-                        if (masked) {
-                            clean_own(dst, item);
+                                for (int n = 0; n < AC_TK / STEP; ++n)
+                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, false, item);
+                            }
+                            mbar_arrive(raw_empty + rslot);
                             fence_proxy_async_smem();
+                            mbar_arrive(full + slot);
+                            if (++rslot == NRAW) {
+                                rslot = 0;
+                                rph ^= 1;
+                            }
+                        } else if (kv) {  // every V tile passes through here, so that the phases cannot run apart
+                            ok = mbar_wait_fast(full + slot, ph, 23, slot);
+                            if (!ok) break;
+                            if (masked) {
+                                clean_own(dst, item);
+                                fence_proxy_async_smem();
+                            }
+                            mbar_arrive(cleaned + slot);
                         }
-                        mbar_arrive(cleaned + slot);
                     }
-                    step2(slot, ph, NS);
                 }
             }
         } else {
