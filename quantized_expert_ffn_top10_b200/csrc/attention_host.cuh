@@ -102,8 +102,9 @@ cudaError_t attn_attrs() {
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 1, 4>, AttCfg<D, F8, 2, 1, 4>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 2, 2>, AttCfg<D, F8, 2, 2, 2>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_rows<D, F8, 2, 4, 2>, AttCfg<D, F8, 2, 4, 2>::SMEM);
-    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, false>, AcCfg<D, F8>::SMEM);
-    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, true>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 0>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 1>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 2>, AcCfg<D, F8>::SMEM);
     return e;
 }
 
@@ -174,8 +175,10 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     const int grid = std::min(sms, ATT_MAX_SMS);
     CUtensorMap tk{}, tv{};
     a.tma = tmap_cache<D, F8>(&tk, a.k, a) && tmap_cache<D, F8>(&tv, a.v, a);
-    if (a.slopes && a.softcap == 0.f) k_attn_chunk<D, F8, true><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
-    else k_attn_chunk<D, F8, false><<<grid, AC_THREADS, AcCfg<D, F8>::SMEM, st>>>(tk, tv, a);
+    constexpr int S = AcCfg<D, F8>::SMEM;
+    if (a.softcap > 0.f && !a.slopes) k_attn_chunk<D, F8, 2><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
+    else if (a.softcap == 0.f && a.slopes) k_attn_chunk<D, F8, 1><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
+    else k_attn_chunk<D, F8, 0><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, sms, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }

@@ -110,8 +110,22 @@ constexpr __host__ __device__ uint32_t ac_idesc(int type, int N, bool b_mn) {
            ((128u >> 4) << 24);
 }
 
-// TILT: slopes without a cap (kept out of the others: its instructions cost them 2%).
-template <int D, bool F8, bool TILT>
+// tanh y = y + y^3 q(y^2) for |y| <= 0.7, q a least-squares fit at Chebyshev nodes: within 4.6e-8 in fp32.
+__device__ __forceinline__ float2 tanh_small2(float2 y) {
+    const float2 zero = make_float2(0.f, 0.f);
+    auto both = [](float c) { return make_float2(c, c); };
+    const float2 z = fma2(y, y, zero);
+    float2 q = fma2(z, both(0.0018368171295151114f), both(-0.007793231401592493f));
+    q = fma2(q, z, both(0.02151893451809883f));
+    q = fma2(q, z, both(-0.05390692502260208f));
+    q = fma2(q, z, both(0.1333281248807907f));
+    q = fma2(q, z, both(-0.33333316445350647f));
+    return fma2(fma2(y, z, zero), q, y);
+}
+
+// MODE: scores that are not S times a number but can be made in registers, kept out of the others' code (its
+// instructions cost them 2%): 1 slopes without a cap, 2 a cap without slopes.
+template <int D, bool F8, int MODE>
 __global__ void __launch_bounds__(AC_THREADS, 1)
     k_attn_chunk(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
     using C = AcCfg<D, F8>;
@@ -279,20 +293,49 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     tc_fence_after();
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
                     const bool masked = __any_sync(~0u, k0 < lo || k0 > hi - AC_TK), edit = masked || !simple;
-                    const bool tilted = TILT && !masked && !__any_sync(~0u, mine && k0 + AC_TK - 1 > pos);
+                    const bool tilted = MODE == 1 && !masked && !__any_sync(~0u, mine && k0 + AC_TK - 1 > pos);
                     // Scores that are not S times a number, or hidden ones, are put in S's place first; but a slope
                     // alone is linear in the column of a tile behind the row, and is added to the registers below.
-                    if (edit && !tilted) {
+                    uint32_t u[128];
+                    auto load_s = [&] {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) tmem_ld32(t_s + g * 32, u + g * 32);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) reg_tie32(u + g * 32);
+                    };
+                    bool capped = false;
+                    if (MODE == 2 && !masked) {  // all scores well below the cap: a polynomial, no special functions
+                        load_s();
+                        float far[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int c = 0; c < 128; c += 2) {
+                            far[0] = fmaxf(far[0], fabsf(__uint_as_float(u[c])));
+                            far[1] = fmaxf(far[1], fabsf(__uint_as_float(u[c + 1])));
+                        }
+                        const float y = rs / a.softcap;
+                        capped = __all_sync(~0u, !mine || fmaxf(far[0], far[1]) * fabsf(y) <= 0.7f);
+                        if (capped) {
+                            const float2 y2 = make_float2(y, y), zero = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int c = 0; c < 128; c += 2) {
+                                const float2 x = tanh_small2(fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), y2, zero));
+                                u[c] = __float_as_uint(x.x);
+                                u[c + 1] = __float_as_uint(x.y);
+                            }
+                        }
+                    }
+                    if (edit && !tilted && !capped) {
                         const int f = masked ? lo - k0 : -1024, e = masked ? hi - k0 : 1024;  // visible columns [f, e)
                         const float p0 = (float)(pos - k0);
 #pragma unroll 1
                         for (int g = 0; g < 128; g += 16) {
-                            uint32_t u[16];
-                            tmem_ld16(t_s + g, u);
-                            tmem_ld_wait16(u);
+                            uint32_t v[16];
+                            tmem_ld16(t_s + g, v);
+                            tmem_ld_wait16(v);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
-                                float x = __uint_as_float(u[c]);
+                                float x = __uint_as_float(v[c]);
                                 if (!simple) {
                                     x *= rs;
                                     if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
@@ -301,18 +344,13 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                                     }
                                     x -= slope * fabsf(p0 - (float)(g + c));
                                 }
-                                u[c] = g + c >= f && g + c < e ? __float_as_uint(x) : 0xff800000u;  // -inf
+                                v[c] = g + c >= f && g + c < e ? __float_as_uint(x) : 0xff800000u;  // -inf
                             }
-                            tmem_st16(t_s + g, u);
+                            tmem_st16(t_s + g, v);
                         }
                         tmem_st_wait();
                     }
-                    uint32_t u[128];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) tmem_ld32(t_s + g * 32, u + g * 32);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) reg_tie32(u + g * 32);
+                    if (!capped) load_s();
                     if (tilted) {
                         const float2 rs2 = make_float2(rs, rs), step = make_float2(2.f * slope, 2.f * slope);
                         const float at0 = -slope * (float)(pos - k0);
@@ -329,7 +367,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 128; c += 2)
                         t4[(c >> 1) & 3] = fmaxf(t4[(c >> 1) & 3], fmaxf(__uint_as_float(u[c]), __uint_as_float(u[c + 1])));
-                    const float mul = simple ? rs : 1.f;
+                    const float mul = simple ? rs : capped ? cap_out : 1.f;
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
                     const bool grew = top > m + GROW || (m == -INFINITY && top > m);
                     if (__any_sync(~0u, grew)) {

@@ -56,13 +56,14 @@ def rope_ref(x, position, inv_freq, rot, interleaved, rot_scale, norm, eps):
 
 
 def attn_ref(q, keys, values, q_len, kv_len, scale, softcap=0.0, window=0, slopes=None, prefix=None):
-    """(out, lse, weight, slack) in fp64: q [T, Hq, D]; keys, values: per request
+    """(out, lse, weight, slack, most) in fp64: q [T, Hq, D]; keys, values: per request
     [kv, Hk, D].  weight = sum_j softmax_j |v_j| (what a relative error of the
     numerators scales with); slack [T, Hq] = the largest sum_d |q_d k_jd| * scale
-    over visible keys (what a relative error of the scores scales with)."""
+    over visible keys (what a relative error of the scores scales with); most = the
+    largest |v_j| of the request's keys."""
     T, Hq, D = q.shape
     out, lse = np.zeros((T, Hq, D)), np.full((T, Hq), -np.inf)
-    weight, slack = np.zeros((T, Hq, D)), np.zeros((T, Hq))
+    weight, slack, most = np.zeros((T, Hq, D)), np.zeros((T, Hq)), np.zeros((T, Hq, D))
     t = 0
     for b, n in enumerate(q_len):
         kv = int(kv_len[b])
@@ -89,26 +90,30 @@ def attn_ref(q, keys, values, q_len, kv_len, scale, softcap=0.0, window=0, slope
                 tot = e.sum(1, keepdims=True)
                 out[sl, h] = e @ v / tot
                 weight[sl, h] = e @ np.abs(v) / tot
+                most[sl, h] = np.abs(v).max(0)
                 lse[sl, h] = (m + np.log(tot))[:, 0]
         t += n
-    return out, lse, weight, slack
+    return out, lse, weight, slack, most
 
 
 def attn_limits(ref, D, n_keys, e4m3):
     """Bounds of |out - ref| and |lse - ref|, counted in roundings.
 
     out: its own rounding to bf16, 2^-8 of the value; the numerators' rounding
-    to bf16 2^-8 (fp16, e4m3 caches: 2^-11, and for what falls below fp16's
-    normal steps half of its smallest, 2^-25, with the numerators lifted by 2^6
-    at least: 2^-31 of a numerator's reference for each key) of the weight; the fp32 sum over the keys, each
+    to bf16 2^-8 (fp16, e4m3 caches: 2^-11) of the weight; for e4m3 caches also
+    what falls below fp16's normal steps: there a numerator, lifted by 2^6 at
+    least, is off by half of fp16's smallest, 2^-25, which is 2^-31 of its
+    reference, and meets |v_j|, not the weighted mean of |v| (which is far smaller
+    where the keys that matter hold a zero), so the n keys are off by n 2^-31
+    max |v| over a sum of at least 1; the fp32 sum over the keys, each
     step cut or rounded to 2^-23; and a score error ds, which moves every
     softmax weight by at most 2 ds.  ds: D products summed in fp32 at 2^-23 a
     step, scaling and base-2 exponent of the score itself (|s| <= slack) at a
     few 2^-24, and the exponential at 2^-22."""
-    out, lse, weight, slack = ref
+    out, lse, weight, slack, most = ref
     ds = (D + 16) * 2.0 ** -23 * slack + 2.0 ** -21
-    p = 2.0 ** -11 + n_keys * 2.0 ** -31 if e4m3 else 2.0 ** -8
-    lim = 1.01 * (2.0 ** -8 * np.abs(out) + (p + (2 * ds)[..., None] + n_keys * 2.0 ** -22) * weight) + 1e-30
+    p, floor = (2.0 ** -11, n_keys * 2.0 ** -31 * most) if e4m3 else (2.0 ** -8, 0.0)
+    lim = 1.01 * (2.0 ** -8 * np.abs(out) + (p + (2 * ds)[..., None] + n_keys * 2.0 ** -22) * weight + floor) + 1e-30
     return lim, ds + n_keys * 2.0 ** -23 + np.where(np.isfinite(lse), np.abs(lse), 0) * 2.0 ** -22
 
 

@@ -97,6 +97,7 @@ SHAPES = [
     dict(q_len=[8] * 12, kv_len=[128 * i + i for i in range(1, 13)], Hq=32, Hk=2, page=8, one_buffer=True),
 ]
 EXTRAS = [
+    dict(softcap=50.0, q_gain=0.5), dict(softcap=50.0, q_gain=40.0, f8=True),  # far below the cap, and far above
     dict(), dict(f8=True), dict(f8=True, scales=False, softcap=20.0), dict(softcap=15.0, window=37), dict(slopes=True),
     dict(window=1), dict(f8=True, slopes=True, window=100),
 ]
