@@ -185,11 +185,11 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
 // Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 16 the row
 // kernels read the cache at memory speed and waste no tensor work on absent rows (64 requests of 8 rows
 // at 32K: 185 us, the chunk kernel 383; of 16 rows at 16K: 242 us, 278).  Above, the chunk kernel does
-// (48 windows of 24 rows at 20K: 144 us, row kernel 196; 64 of 40 rows at 16K: 300 us, 520), except
+// (48 windows of 24 rows at 20K: 144 us, row kernel 196; 64 of 40 rows at 16K: 305 us, 520), except
 // that it takes longer to start and end, so a small call (query rows x keys the table can hold below
 // 2^19) stays with the row kernels (5 tokens of 8 heads a cached one at 1,000 keys: 15.4 us, the chunk
 // kernel 22; 37 tokens at 8,192: 39 us, 34), and that capped scores cost it more (24 windows of 25 rows
-// in a 4K sliding window: 89 us, 97).
+// in a 4K sliding window: 89 us, 110).
 template <int D, bool F8>
 cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     const int64_t rows = (int64_t)std::min(a.max_q, a.T) * a.G;
