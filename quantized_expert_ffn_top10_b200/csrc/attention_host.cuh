@@ -215,7 +215,10 @@ int run_attn(const AttnCall& c) {
     a.page_b = d->page_stride * es; a.token_b = d->token_stride * es; a.head_b = d->head_stride * es;
     a.n_pages = d->n_pages; a.page_size = d->page_size;
     a.cu = c.cu; a.kv_len = c.kv_len; a.table = c.table; a.width = c.width;
-    a.T = c.T; a.B = c.B; a.Hk = d->n_kv_heads; a.G = d->n_heads / d->n_kv_heads; a.max_q = c.max_q; a.window = c.window;
+    a.T = c.T; a.B = c.B; a.Hk = d->n_kv_heads; a.G = d->n_heads / d->n_kv_heads; a.max_q = c.max_q;
+    // a window of all the keys there can be is none, and below it `position - window` stays within 32 bits
+    // (positions are negative for rows before the first key)
+    a.window = c.window >= MOE_ATTN_MAX_KV ? 0 : c.window;
     a.scale = c.scale; a.softcap = c.softcap; a.slopes = c.slopes; a.prefix = c.prefix;
     a.out = c.out; a.lse = c.lse;
     a.hdr = reinterpret_cast<int4*>(c.ws + L.hdr);

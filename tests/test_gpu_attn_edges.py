@@ -1,0 +1,48 @@
+"""Calls at the edges of what the attention half takes: each test holds one
+property of the row kernels and, with a block table wide enough that the call
+counts as a large one, of the chunk kernel."""
+import numpy as np
+import pytest
+
+import quantized_expert_ffn_top10_b200 as M
+from attn_ref import attn_limits, bf16
+from test_gpu_attn import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def wide(c, keys=1 << 16):
+    """The case's table with room for so many keys (the columns behind its pages hold no page)."""
+    import torch
+    t = c.cache.table_dev
+    cols = max(t.shape[1], -(-keys // c.cache.page))
+    out = torch.full((t.shape[0], cols), -1, dtype=torch.int32, device="cuda")
+    out[:, :t.shape[1]] = t
+    return out
+
+
+def check_rows(c, rows, ref=None):
+    """The rows [rows] of the step against the reference."""
+    import torch
+    torch.cuda.synchronize()
+    ref = ref or c.ref()
+    lim, lse_lim = attn_limits(ref, c.D, max(c.kv_len), c.f8)
+    got, lse = c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    assert np.all(np.abs(got - ref[0])[rows] <= lim[rows])
+    with np.errstate(invalid="ignore"):
+        off = np.abs(lse - ref[1])
+    assert np.all((off <= lse_lim)[rows] | np.isneginf(ref[1])[rows])
+    assert np.array_equal(np.isneginf(lse)[rows], np.isneginf(ref[1])[rows])
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, 1 << 30, (1 << 30) - 1])
+@pytest.mark.parametrize("which,page", [("decode", 16), ("prefill", 16), ("prefill", 24)])
+def test_widest_windows(cuda_ok, which, page, window):
+    """The largest window there is means no window, also for rows before the
+    first key (requests with fewer keys than new rows)."""
+    c = Case([5, 5, 5, 5], [0, 2, 40, 3], Hq=8, Hk=1, page=page, window=window, seed=50)
+    c.run(which)
+    c.check()
+    c.out.fill_(7.0)
+    c.run(which, table=wide(c))
+    c.check()
