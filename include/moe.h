@@ -347,11 +347,12 @@ typedef struct moe_kv_desc {
  * n_free (requests are served in order), gets no page: slots -1, kv_len_new =
  * kv_len, MOE_ERR_PAGES latched; attention over its new rows is then not
  * meaningful.  A negative length counts as 0, and rows past T are dropped,
- * with MOE_ERR_RANGE latched; a token whose page is negative or past the slot
- * range gets slot -1 with MOE_ERR_SLOT.  All int32.  0 <= B <= MOE_ATTN_MAX_B,
- * 0 <= T <= MOE_KV_MAP_MAX_T, page_size, table_width >= 1.  No output may
- * overlap an input or another output (MOE_ERR_ARG): the lengths are not updated
- * in place.
+ * with MOE_ERR_RANGE latched (kv_len_new counts dropped rows too, so attention
+ * over a request that lost some is not meaningful either); a token whose page is
+ * negative or past the slot range gets slot -1 with MOE_ERR_SLOT.  All int32.
+ * 0 <= B <= MOE_ATTN_MAX_B, 0 <= T <= MOE_KV_MAP_MAX_T, page_size, table_width
+ * >= 1.  No output may overlap an input or another output (MOE_ERR_ARG): the
+ * lengths are not updated in place.
  */
 int moe_kv_map(const int32_t* kv_len, const int32_t* q_len, int B, int page_size, const int32_t* free_pages, int n_free,
                int32_t* block_table, int table_width, int T, int32_t* kv_len_new, int32_t* cu_q, int32_t* position,
@@ -426,9 +427,10 @@ size_t moe_attn_workspace_bytes(int T, int B, int n_heads, int n_kv_heads, int h
  * rounded to 16 bits (bf16, or fp16 for an E4M3 cache) for the product with v.
  * Values behind kv_len or hidden by the mask are never used, NaN or not.  The
  * lengths are read on the device only, so a captured call replays with new
- * ones.  Rows past max_q of a request and lengths past table_width * page_size or
- * MOE_ATTN_MAX_KV are not read; a page id outside the cache reads as zeros and latches
- * MOE_ERR_SLOT.  Results do not depend on timing.
+ * ones.  Offsets count as cut to [0, T]; rows past max_q of a request are left as
+ * they were, and its others keep the positions above; lengths past table_width *
+ * page_size or MOE_ATTN_MAX_KV are not read; a page id outside the cache reads as
+ * zeros and latches MOE_ERR_SLOT.  Results do not depend on timing.
  */
 int moe_attn_decode(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride, int T, const int32_t* cu_q,
                     const int32_t* kv_len, int B, const int32_t* block_table, int table_width, int max_q, float scale,

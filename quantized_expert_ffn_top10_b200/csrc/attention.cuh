@@ -1,5 +1,5 @@
 // Attention over the paged key-value cache.  For a query row (token i of
-// request b, head) at position pos = kv_len - n_new + i, over its visible keys
+// request b, head) at position pos = kv_len - n_new + i (n_new: all its rows in the step), over its visible keys
 // j in [lo, hi), hi = max(pos + 1, min(prefix, kv_len)), lo = max(0, pos - W + 1):
 //   s_j = scale q . k_j, capped: cap tanh(s_j / cap), less slope |pos - j|
 //   out = sum_j exp(s_j) v_j / sum_j exp(s_j),  lse = log sum_j exp(s_j).
@@ -112,20 +112,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 
 // A request's rows and lengths, with every device-side number clamped to what the call's arguments allow.
+// Positions go by all the rows that the offsets give the request, also where only max_q of them are taken.
 struct AttSeq {
-    int t0, n, kv, pre;
+    int t0, n, p0, pre;  // first row, rows, position of the first, end of the prefix
 };
 __device__ __forceinline__ AttSeq att_seq(const AttnArgs& a, int b) {
     AttSeq s;
     s.t0 = min(max(a.cu[b], 0), a.T);
-    s.n = min(min(max(a.cu[b + 1], s.t0), a.T) - s.t0, a.max_q);
-    s.kv = min(max(a.kv_len[b], 0), (int)min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV));
-    s.pre = a.prefix ? min(max(a.prefix[b], 0), s.kv) : 0;
+    const int rows = min(max(a.cu[b + 1], s.t0), a.T) - s.t0;
+    const int kv = min(max(a.kv_len[b], 0), (int)min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV));
+    s.n = min(rows, a.max_q);
+    s.p0 = kv - rows;
+    s.pre = a.prefix ? min(max(a.prefix[b], 0), kv) : 0;
     return s;
 }
 // visible keys [lo, hi) of token i of the request
 __device__ __forceinline__ void att_range(const AttnArgs& a, const AttSeq& s, int i, int& lo, int& hi) {
-    const int pos = s.kv - s.n + i;
+    const int pos = s.p0 + i;
     hi = max(max(pos + 1, s.pre), 0);
     lo = a.window ? max(0, pos - a.window + 1) : 0;
 }
@@ -237,7 +240,7 @@ __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, At
     int64_t mine = 0, entries;
     for (int b = b0; b < b1; ++b) {
         const AttSeq s = att_seq(a, b);
-        if (b < kept) seq[b] = make_int4(s.t0, s.n, s.kv, s.pre);
+        if (b < kept) seq[b] = make_int4(s.t0, s.n, s.p0, s.pre);
         mine += ((int64_t)s.n * a.G + ROWS - 1) / ROWS;
     }
     int64_t ex = scan(mine, entries);
@@ -483,7 +486,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                     const int r2 = (rw * NTW + nt) * 8 + qd * 2 + j, rr2 = cur.rt * ROWS + r2;
                     rs[nt][j] = a.scale * ks * __shfl_sync(~0u, unit, (qd * 2 + j) * 4) * (a.softcap > 0.f ? 1.f : LOG2E);
                     rlo[nt][j] = rhi[nt][j] = 0;
-                    rpos[nt][j] = cur.s.kv - cur.s.n + rr2 / a.G;
+                    rpos[nt][j] = cur.s.p0 + rr2 / a.G;
                     slope[nt][j] = 0.f;
                     if (r2 < rows) {
                         att_range(a, cur.s, rr2 / a.G, rlo[nt][j], rhi[nt][j]);

@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             const bool mine = row0 + r < rows, busy = __any_sync(~0u, mine);  // a warp without rows only keeps step
             int lo = 0, hi = 0x7fffffff;  // (a lane without a row must not make its warp mask)
             if (mine) att_range(a, cur.s, i, lo, hi);
-            const int pos = cur.s.kv - cur.s.n + i;
+            const int pos = cur.s.p0 + i;
             const float ks = (F8 && a.k_scale) ? __ldg(a.k_scale + cur.h) : 1.f;
             const float vs = (F8 && a.v_scale) ? __ldg(a.v_scale + cur.h) : 1.f;
             const bool simple = a.softcap == 0.f && !a.slopes && a.scale * ks > 0.f;  // scores are S times a positive number

@@ -46,3 +46,17 @@ def test_widest_windows(cuda_ok, which, page, window):
     c.out.fill_(7.0)
     c.run(which, table=wide(c))
     c.check()
+
+
+@pytest.mark.parametrize("extra", [dict(), dict(window=7), dict(slopes=True)])
+@pytest.mark.parametrize("tables", ["tight", "wide"])
+def test_rows_of_a_wider_request_keep_their_positions(cuda_ok, tables, extra):
+    """A request that brings more rows than max_q: the first max_q rows are
+    those of the whole request, the others stay as they were."""
+    c = Case([3, 1, 6], [40, 9, 300], Hq=16, Hk=1, page=16, seed=51, **extra)
+    c.run("decode", max_q=2, table=wide(c) if tables == "wide" else None)
+    rows = [0, 1, 3, 4, 5]
+    check_rows(c, rows)
+    left = [2, 6, 7, 8, 9]
+    assert bool((c.out[left] == 7.0).all()) and bool((c.lse[left] == 7.0).all())
+    assert M.moe_last_device_error() == 0
