@@ -49,6 +49,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // two fp32 at once
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
     float2 r;
@@ -64,6 +70,25 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
     return r;
 }
+
+__device__ __forceinline__ float2 both(float c) { return make_float2(c, c); }
+
+// The cap of a base-2 score x, cap tanh(x / cap).  For y = x / cap up to 0.35 it is x + x z q(z), z = y^2, q a least-
+// squares fit of tanh at Chebyshev nodes, within 9.9e-8 of y in fp32: the error is the score's own rounding whatever
+// the cap (z = 0 leaves x as it is).  Above, cap (1 - 2 / (1 + e^2y)), whose error is 2^-23 of the cap, there of the
+// score's size.  (For small y it would not be: 1e-7 of a cap of 1e6 is 0.1.)
+struct AttCap {
+    float in, out;  // ln 2 / cap (so that y = x in), cap log2 e
+    __device__ __forceinline__ explicit AttCap(float cap) : in(0.6931471805599453f / cap), out(cap * 1.4426950408889634f) {}
+    __device__ __forceinline__ float2 operator()(float2 x) const {
+        const float2 y = fma2(x, both(in), both(0.f)), z = fma2(y, y, both(0.f));
+        float2 q = fma2(z, both(-0.04913432523608208f), both(0.13299560546875f));
+        q = fma2(q, z, both(-0.333326518535614f));
+        q = fma2(fma2(x, z, both(0.f)), q, x);
+        auto large = [&](float v) { return fmaf(-2.f * out, rcp_approx(1.f + ex2(v * (2.f * 1.4426950408889634f))), out); };
+        return make_float2(fabsf(y.x) <= 0.35f ? q.x : large(y.x), fabsf(y.y) <= 0.35f ? q.y : large(y.y));
+    }
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -423,7 +448,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
     int rlo[NTW][2], rhi[NTW][2], rpos[NTW][2];
     int all_lo = 0, all_hi = 0;  // keys that every row of the tile sees
     const bool extra = a.softcap > 0.f || a.slopes;
-    const float cap_in = 2.f * LOG2E / a.softcap, cap_out = a.softcap * LOG2E;
+    const AttCap cap(a.softcap);
     float vs = 1.f;
     bool started = false;
 
@@ -484,7 +509,7 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {  // the rows of this lane's accumulators
                     const int r2 = (rw * NTW + nt) * 8 + qd * 2 + j, rr2 = cur.rt * ROWS + r2;
-                    rs[nt][j] = a.scale * ks * __shfl_sync(~0u, unit, (qd * 2 + j) * 4) * (a.softcap > 0.f ? 1.f : LOG2E);
+                    rs[nt][j] = a.scale * ks * __shfl_sync(~0u, unit, (qd * 2 + j) * 4) * LOG2E;
                     rlo[nt][j] = rhi[nt][j] = 0;
                     rpos[nt][j] = cur.s.p0 + rr2 / a.G;
                     slope[nt][j] = 0.f;
@@ -553,15 +578,21 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
-                            float x = s[nt][u][e] * rs[nt][j];
-                            if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
-                                const float y = ex2(x * cap_in);
-                                x = cap_out * (1.f - __fdividef(2.f, 1.f + y));
-                            }
-                            s[nt][u][e] = x - slope[nt][j] * fabsf((float)(rpos[nt][j] - key));
+                        for (int e = 0; e < 4; e += 2) {
+                            float2 x = make_float2(s[nt][u][e] * rs[nt][0], s[nt][u][e + 1] * rs[nt][1]);
+                            if (a.softcap > 0.f) x = cap(x);
+                            s[nt][u][e] = x.x;
+                            s[nt][u][e + 1] = x.y;
                         }
+                    if (a.slopes) {
+#pragma unroll
+                        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = e & 1, key = k0 + kr + u * 16 + g8 + (e >> 1) * 8;
+                                s[nt][u][e] -= slope[nt][j] * fabsf((float)(rpos[nt][j] - key));
+                            }
+                    }
                 } else {
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)

@@ -105,6 +105,7 @@ cudaError_t attn_attrs() {
     if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 0>, AcCfg<D, F8>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 1>, AcCfg<D, F8>::SMEM);
     if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 2>, AcCfg<D, F8>::SMEM);
+    if (e == cudaSuccess) e = set_smem(k_attn_chunk<D, F8, 3>, AcCfg<D, F8>::SMEM);
     return e;
 }
 
@@ -176,9 +177,12 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
     CUtensorMap tk{}, tv{};
     a.tma = tmap_cache<D, F8>(&tk, a.k, a) && tmap_cache<D, F8>(&tv, a.v, a);
     constexpr int S = AcCfg<D, F8>::SMEM;
-    if (a.softcap > 0.f && !a.slopes) k_attn_chunk<D, F8, 2><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
-    else if (a.softcap == 0.f && a.slopes) k_attn_chunk<D, F8, 1><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
-    else k_attn_chunk<D, F8, 0><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
+    switch ((a.softcap > 0.f ? 2 : 0) | (a.slopes ? 1 : 0)) {
+        case 0: k_attn_chunk<D, F8, 0><<<grid, AC_THREADS, S, st>>>(tk, tv, a); break;
+        case 1: k_attn_chunk<D, F8, 1><<<grid, AC_THREADS, S, st>>>(tk, tv, a); break;
+        case 2: k_attn_chunk<D, F8, 2><<<grid, AC_THREADS, S, st>>>(tk, tv, a); break;
+        default: k_attn_chunk<D, F8, 3><<<grid, AC_THREADS, S, st>>>(tk, tv, a);
+    }
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? launch_attn_join<D>(a, sms, grid, AC_ROWS, F8 ? 6.f : 0.f, st) : e;
 }

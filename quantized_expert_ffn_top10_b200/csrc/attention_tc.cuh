@@ -110,21 +110,16 @@ constexpr __host__ __device__ uint32_t ac_idesc(int type, int N, bool b_mn) {
            ((128u >> 4) << 24);
 }
 
-// tanh y = y + y^3 q(y^2) for |y| <= 0.7, q a least-squares fit at Chebyshev nodes: within 4.6e-8 in fp32.
-__device__ __forceinline__ float2 tanh_small2(float2 y) {
-    const float2 zero = make_float2(0.f, 0.f);
-    auto both = [](float c) { return make_float2(c, c); };
-    const float2 z = fma2(y, y, zero);
+// tanh y / y - 1 = z q(z), z = y^2, for |y| <= 0.7: q a least-squares fit at Chebyshev nodes, within 4.6e-8 in fp32.
+__device__ __forceinline__ float2 ac_cap_poly2(float2 z) {
     float2 q = fma2(z, both(0.0018368171295151114f), both(-0.007793231401592493f));
     q = fma2(q, z, both(0.02151893451809883f));
     q = fma2(q, z, both(-0.05390692502260208f));
     q = fma2(q, z, both(0.1333281248807907f));
-    q = fma2(q, z, both(-0.33333316445350647f));
-    return fma2(fma2(y, z, zero), q, y);
+    return fma2(q, z, both(-0.33333316445350647f));
 }
 
-// MODE: scores that are not S times a number but can be made in registers, kept out of the others' code (its
-// instructions cost them 2%): 1 slopes without a cap, 2 a cap without slopes.
+// MODE: 1 slopes, 2 a cap, 3 both.  Each is kept out of the others' code, whose instructions would cost them 2 to 3%.
 template <int D, bool F8, int MODE>
 __global__ void __launch_bounds__(AC_THREADS, 1)
     k_attn_chunk(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const AttnArgs a) {
@@ -238,8 +233,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             const int pos = cur.s.p0 + i;
             const float ks = (F8 && a.k_scale) ? __ldg(a.k_scale + cur.h) : 1.f;
             const float vs = (F8 && a.v_scale) ? __ldg(a.v_scale + cur.h) : 1.f;
-            const bool simple = a.softcap == 0.f && !a.slopes && a.scale * ks > 0.f;  // scores are S times a positive number
-            const float slope = (a.slopes && mine) ? __ldg(a.slopes + head) * LOG2E : 0.f;
+            const bool simple = MODE == 0 && a.scale * ks > 0.f;  // scores are S times a positive number
+            const float slope = ((MODE & 1) && mine) ? __ldg(a.slopes + head) * LOG2E : 0.f;
             // ---- Q: this warp's 32 rows into the half's K-major operand tile, LPR lanes to a row.  The loops
             // that run once an item are kept short: unrolled, they cost more in instruction fetches.
             constexpr int LPR = D / 8, RPI = 32 / LPR;
@@ -282,8 +277,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
-            const float rs = a.scale * ks * unit * (a.softcap > 0.f ? 1.f : LOG2E);
-            const float cap_in = 2.f * LOG2E / a.softcap, cap_out = a.softcap * LOG2E;
+            const float rs = a.scale * ks * unit * LOG2E;
+            const AttCap cap(a.softcap);
             float m = -INFINITY, l = 0.f;
             for (int n = 0; n < steps; ++n) {
                 const int j = duo ? 2 * n + half : n;
@@ -313,15 +308,17 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             far[0] = fmaxf(far[0], fabsf(__uint_as_float(u[c])));
                             far[1] = fmaxf(far[1], fabsf(__uint_as_float(u[c + 1])));
                         }
-                        const float y = rs / a.softcap;
-                        capped = __all_sync(~0u, !mine || fmaxf(far[0], far[1]) * fabsf(y) <= 0.7f);
+                        // u becomes S (1 + z q(z)), z = (S rs / cap)^2, still to be multiplied by rs
+                        const float y = rs * cap.in;
+                        capped = __all_sync(~0u, !mine || (rs > 0.f && fmaxf(far[0], far[1]) * y <= 0.7f));
                         if (capped) {
-                            const float2 y2 = make_float2(y, y), zero = make_float2(0.f, 0.f);
+                            const float2 y2 = both(y), zero = both(0.f), one = both(1.f);
 #pragma unroll
                             for (int c = 0; c < 128; c += 2) {
-                                const float2 x = tanh_small2(fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), y2, zero));
-                                u[c] = __float_as_uint(x.x);
-                                u[c + 1] = __float_as_uint(x.y);
+                                const float2 x = make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), t = fma2(x, y2, zero),
+                                             z = fma2(t, t, zero), r = fma2(x, fma2(z, ac_cap_poly2(z), one), zero);
+                                u[c] = __float_as_uint(r.x);
+                                u[c + 1] = __float_as_uint(r.y);
                             }
                         }
                     }
@@ -334,17 +331,18 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             tmem_ld16(t_s + g, v);
                             tmem_ld_wait16(v);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                float x = __uint_as_float(v[c]);
+                            for (int c = 0; c < 16; c += 2) {
+                                float2 x = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
                                 if (!simple) {
-                                    x *= rs;
-                                    if (a.softcap > 0.f) {  // cap tanh(x / cap), tanh y = 1 - 2 / (1 + e^2y)
-                                        const float y = ex2(x * cap_in);
-                                        x = cap_out * (1.f - __fdividef(2.f, 1.f + y));
+                                    x = make_float2(x.x * rs, x.y * rs);
+                                    if constexpr ((MODE & 2) != 0) x = cap(x);
+                                    if constexpr ((MODE & 1) != 0) {
+                                        x.x -= slope * fabsf(p0 - (float)(g + c));
+                                        x.y -= slope * fabsf(p0 - (float)(g + c + 1));
                                     }
-                                    x -= slope * fabsf(p0 - (float)(g + c));
                                 }
-                                v[c] = g + c >= f && g + c < e ? __float_as_uint(x) : 0xff800000u;  // -inf
+                                v[c] = g + c >= f && g + c < e ? __float_as_uint(x.x) : 0xff800000u;  // -inf
+                                v[c + 1] = g + c + 1 >= f && g + c + 1 < e ? __float_as_uint(x.y) : 0xff800000u;
                             }
                             tmem_st16(t_s + g, v);
                         }
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < 128; c += 2)
                         t4[(c >> 1) & 3] = fmaxf(t4[(c >> 1) & 3], fmaxf(__uint_as_float(u[c]), __uint_as_float(u[c + 1])));
-                    const float mul = simple ? rs : capped ? cap_out : 1.f;
+                    const float mul = simple || capped ? rs : 1.f;
                     const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * mul;
                     const bool grew = top > m + GROW || (m == -INFINITY && top > m);
                     if (__any_sync(~0u, grew)) {

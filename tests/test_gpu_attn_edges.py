@@ -60,3 +60,28 @@ def test_rows_of_a_wider_request_keep_their_positions(cuda_ok, tables, extra):
     left = [2, 6, 7, 8, 9]
     assert bool((c.out[left] == 7.0).all()) and bool((c.lse[left] == 7.0).all())
     assert M.moe_last_device_error() == 0
+
+
+@pytest.mark.parametrize("softcap", [1e3, 1e4, 1e6, 1e8, 1e20, 1e30, 3e38])
+@pytest.mark.parametrize("extra", [dict(), dict(f8=True), dict(slopes=True), dict(window=200)])
+@pytest.mark.parametrize("which", ["decode", "decode16", "prefill", "chunk"])
+def test_large_caps(cuda_ok, which, extra, softcap):
+    """A cap far above the scores changes them by less than their rounding: the
+    cap's own arithmetic adds a few 2^-24 of the score (the limits' 16 steps)."""
+    if which in ("decode", "decode16"):
+        c = Case([1, 5], [300, 77], Hq=6 if which == "decode" else 24, Hk=2, page=16, softcap=softcap, seed=52, **extra)
+        c.run("decode")
+    else:
+        c = Case([140, 33], [900, 33], Hq=4, Hk=2, page=16, softcap=softcap, seed=53, **extra)
+        c.run("prefill", table=wide(c) if which == "chunk" else None)
+    c.check()
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("q_gain", [0.3, 6.0, 40.0])
+@pytest.mark.parametrize("f8", [False, True])
+def test_caps_and_slopes_of_the_chunk_kernel(cuda_ok, f8, q_gain, slopes):
+    """Scores below, around and above the cap, hidden or not, with slopes and without."""
+    c = Case([300, 45], [1500, 45], Hq=4, Hk=1, page=16, softcap=12.0, q_gain=q_gain, slopes=slopes, f8=f8, seed=54)
+    c.run("prefill", table=wide(c))
+    c.check()
