@@ -160,24 +160,25 @@ __device__ __forceinline__ void att_range(const AttnArgs& a, const AttSeq& s, in
 
 // An item's position in the deal: row tile rt of request b for cached head h, key tile `tile` of n.
 struct AttCur {
-    int b, rt, h, tile, n, lo, hi;
+    int b, rt, h, tile, n, lo, hi;  // lo: where the key tiles start
+    int first;                      // the first key that a row sees (lo rounded up again)
     AttSeq s;
 };
 
 // Key tiles of a row tile; they start at the first visible key, or at the multiple of ALIGN at or before it.
 template <int ROWS, int TK, int ALIGN>
-__device__ __forceinline__ int att_tiles(const AttnArgs& a, const AttSeq& s, int rt, int& lo, int& hi) {
+__device__ __forceinline__ int att_tiles(const AttnArgs& a, const AttSeq& s, int rt, int& first, int& lo, int& hi) {
     const int i0 = rt * ROWS / a.G, i1 = min(s.n - 1, (rt * ROWS + ROWS - 1) / a.G);
     int l1, h0;
-    att_range(a, s, i0, lo, h0);
+    att_range(a, s, i0, first, h0);
     att_range(a, s, i1, l1, hi);
-    lo -= lo % ALIGN;
+    lo = first - first % ALIGN;
     return hi > lo ? (hi - lo + TK - 1) / TK : 1;  // a row tile without a key still has its rows to write
 }
 
 template <int ROWS, int TK, int ALIGN>
 __device__ __forceinline__ void att_enter(const AttnArgs& a, AttCur& c) {
-    c.n = att_tiles<ROWS, TK, ALIGN>(a, c.s, c.rt, c.lo, c.hi);
+    c.n = att_tiles<ROWS, TK, ALIGN>(a, c.s, c.rt, c.first, c.lo, c.hi);
 }
 
 // Next item in the deal's order (cached heads of a row tile, row tiles, requests), and next key tile.
@@ -293,8 +294,8 @@ __device__ __forceinline__ void att_deal(const AttnArgs& a, uint8_t* scratch, At
                 do ++b; while (base[b + 1] <= e);
                 s = get(b);
             }
-            int lo, hi;
-            if (f(b, e - base[b], att_tiles<ROWS, TK, ALIGN>(a, s, e - base[b], lo, hi) + OV)) break;
+            int first, lo, hi;
+            if (f(b, e - base[b], att_tiles<ROWS, TK, ALIGN>(a, s, e - base[b], first, lo, hi) + OV)) break;
         }
     };
     int64_t tiles = 0, all;

@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             bool pg_live = false;
             auto fetch = [&] {
                 const int key = cur.lo + (cur.tile + j) * AC_TK + t;
-                pg_live = key < cur.hi;
+                pg_live = key >= cur.first && key < cur.hi;
                 if (pg_live) {
                     const int col = key / a.page_size;
                     pg_off = key - col * a.page_size;
@@ -783,11 +783,12 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             uint8_t* const base = smem + (F8 ? C::OFF_RAW : C::OFF_RING);
             constexpr uint32_t BYTES = F8 ? C::RAW : TILE;
             int pg = 0, issued = 0, j = 0;
-            // page of box `lane`; past the last key it is never read by a row: any page, or none, serves
+            // page of box `lane`; wholly before the first visible key or past the last one no row reads it, and the
+            // table may hold anything there (pages given back behind a window): none is looked up
             auto fetch = [&] {
                 const int key = cur.lo + (cur.tile + j) * AC_TK + lane * high;
                 pg = -1;
-                if (lane < np && key < cur.hi) {
+                if (lane < np && key + high > cur.first && key < cur.hi) {
                     pg = __ldg(a.table + (int64_t)cur.b * a.width + key / ps);
                     if (pg < 0 || pg >= a.n_pages) {
                         moe_set_status(MOE_ERR_SLOT);  // a box outside the cache reads as zeros

@@ -85,3 +85,25 @@ def test_caps_and_slopes_of_the_chunk_kernel(cuda_ok, f8, q_gain, slopes):
     c = Case([300, 45], [1500, 45], Hq=4, Hk=1, page=16, softcap=12.0, q_gain=q_gain, slopes=slopes, f8=f8, seed=54)
     c.run("prefill", table=wide(c))
     c.check()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("which,page,tables", [("decode", 16, "tight"), ("prefill", 16, "wide"), ("prefill", 24, "wide"),
+                                               ("prefill", 64, "wide"), ("prefill", 1, "wide"), ("prefill", 256, "wide")])
+def test_pages_given_back_behind_a_window(cuda_ok, which, page, tables, f8):
+    """Table entries of pages that no row sees may hold anything: they are
+    neither read nor reported."""
+    import torch
+    q, kv, window = ([5, 3], [1000, 333], 100) if which == "decode" else ([70, 3], [1801, 777], 300)
+    c = Case(q, kv, Hq=8, Hk=2, page=page, window=window, f8=f8, seed=55)
+    table = wide(c) if tables == "wide" else c.cache.table_dev.clone()
+    for b in range(2):
+        first = kv[b] - q[b] - window + 1  # the first key that a row sees
+        gone = torch.tensor([-1, 1 << 30, c.cache.n_pages], dtype=torch.int32, device="cuda")
+        table[b, :first // page] = gone.repeat(first // page // 3 + 1)[:first // page]
+    c.run(which, table=table)
+    c.check()
+    table[0, (kv[0] - 1) // page] = -1  # a page that rows see is still reported
+    c.run(which, table=table)
+    torch.cuda.synchronize()
+    assert M.moe_last_device_error() == M.MOE_ERR_SLOT
