@@ -562,12 +562,14 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         const int t = tid - 256;
         constexpr int CHG = D * (F8 ? 1 : 2) / 16, STEP = 128 / CHG;  // 16-byte pieces of a cached row; rows a pass
         const int c = t % CHG, t_row = t / CHG;
-        auto clean2 = [&](uint32_t x, int item) {  // two 16-bit values, non-finite ones set to zero
+        // two 16-bit values, non-finite ones set to zero; `note` 0: of a key that no row sees (never written, or
+        // behind a window), which need not be added back
+        auto clean2 = [&](uint32_t x, int note) {
             constexpr uint32_t EXP = F8 ? 0x7c00u : 0x7f80u;
             uint32_t keep = ~0u;
             if ((x & EXP) == EXP) keep &= 0xffff0000u;
             if ((x & EXP << 16) == EXP << 16) keep &= 0x0000ffffu;
-            if (keep != ~0u) odd[item & 7] = item + 1;
+            if (keep != ~0u && note) odd[(note - 1) & 7] = note;
             return x & keep;
         };
         // 16 e4m3 values into their two pieces of this thread's first row of a tile; its rows are STEP (a
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
         static_assert(!F8 || STEP % 8 == 0, "the swizzle repeats every 8 rows");
         const bool turn = D == 128 && (c & 4);  // the second block's lanes start with the other piece: no bank twice
         const int at0 = place(t_row, 2 * c + turn), at1 = place(t_row, 2 * c + 1 - turn);
-        auto widen = [&](uint4 w, uint8_t* dst, bool clean, int item) {
+        auto widen = [&](uint4 w, uint8_t* dst, bool clean, int note) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
             uint32_t y[8];
 #pragma unroll
@@ -585,18 +587,19 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             }
             if (clean) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = clean2(y[e], item);
+                for (int e = 0; e < 8; ++e) y[e] = clean2(y[e], note);
             }
             const uint4 p0 = make_uint4(y[0], y[1], y[2], y[3]), p1 = make_uint4(y[4], y[5], y[6], y[7]);
             *reinterpret_cast<uint4*>(dst + at0) = turn ? p1 : p0;
             *reinterpret_cast<uint4*>(dst + at1) = turn ? p0 : p1;
         };
-        auto clean_own = [&](uint8_t* dst, int item) {  // bf16: this thread's pieces of a tile
+        auto clean_own = [&](uint8_t* dst, int seen0, int seen1, int item) {  // bf16: this thread's pieces of a tile, keys seen in [seen0, seen1)
 #pragma unroll 1
             for (int row = t_row; row < AC_TK; row += STEP) {
                 uint4* p = reinterpret_cast<uint4*>(dst + place(row, c));
                 const uint4 w = *p;
-                const uint4 n = make_uint4(clean2(w.x, item), clean2(w.y, item), clean2(w.z, item), clean2(w.w, item));
+                const int note = row >= seen0 && row < seen1 ? item + 1 : 0;
+                const uint4 n = make_uint4(clean2(w.x, note), clean2(w.y, note), clean2(w.z, note), clean2(w.w, note));
                 if (n.x != w.x || n.y != w.y || n.z != w.z || n.w != w.w) *p = n;
             }
         };
@@ -622,12 +625,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             const uint8_t* const src = smem + C::OFF_RAW + rslot * C::RAW + t_row * D + c * 16;
                             if (masked) {
 #pragma unroll 1
-                                for (int n = 0; n < AC_TK / STEP; ++n)
-                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, true, item);
+                                for (int n = 0; n < AC_TK / STEP; ++n) {
+                                    const int key = k0 + t_row + n * STEP;
+                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, true,
+                                          key >= cur.first && key < cur.hi ? item + 1 : 0);
+                                }
                             } else {
 #pragma unroll 4
                                 for (int n = 0; n < AC_TK / STEP; ++n)
-                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, false, item);
+                                    widen(*reinterpret_cast<const uint4*>(src + n * STEP * D), dst + n * STEP * 128, false, 0);
                             }
                             mbar_arrive(raw_empty + rslot);
                             fence_proxy_async_smem();
@@ -640,7 +646,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             ok = mbar_wait_fast(full + slot, ph, 23, slot);
                             if (!ok) break;
                             if (masked) {
-                                clean_own(dst, item);
+                                clean_own(dst, cur.first - k0, cur.hi - k0, item);
                                 fence_proxy_async_smem();
                             }
                             mbar_arrive(cleaned + slot);
@@ -696,14 +702,14 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         const int64_t from = of[row];
                         if constexpr (F8)
                             widen(from >= 0 ? *reinterpret_cast<const uint4*>(src + from) : make_uint4(0, 0, 0, 0),
-                                  dst + (row - t_row) * 128, kv && masked, this_item);
+                                  dst + (row - t_row) * 128, kv && masked, this_item + 1);
                         else
                             cp_async16(smem_u32(dst + place(row, c)), src + (from < 0 ? 0 : from), from >= 0);
                     }
                     if constexpr (!F8) {
                         cp_async_commit();
                         cp_async_wait<0>();
-                        if (kv && masked) clean_own(dst, this_item);
+                        if (kv && masked) clean_own(dst, 0, AC_TK, this_item);  // (a key that no row sees is a row of zeros)
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(full + slot);
