@@ -55,14 +55,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// two fp32 at once
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<uint64_t&>(r))
-        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
-    return r;
-}
 __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     float2 r;
     asm("add.rn.f32x2 %0, %1, %2;"
@@ -70,8 +62,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
     return r;
 }
-
-__device__ __forceinline__ float2 both(float c) { return make_float2(c, c); }
 
 // The cap of a base-2 score x, cap tanh(x / cap).  For y = x / cap up to 0.35 it is x + x z q(z), z = y^2, q a least-
 // squares fit of tanh at Chebyshev nodes, within 9.9e-8 of y in fp32: the error is the score's own rounding whatever

@@ -34,7 +34,7 @@ template <int D, bool F8>
 void launch_rope(const RopeArgs& a, cudaStream_t st) {
     const int tok = a.T >= QR_TOKENS * 4 * 148 ? QR_TOKENS : 1, pieces = tok * (a.Hq + 2 * a.Hk) * (D / 16);
     const int each = tok == 1 ? 1 : QR_UNROLL;  // pieces a thread
-    const int threads = std::min(QR_MAX_THREADS, std::max(64, ((pieces + each - 1) / each + 31) / 32 * 32));
+    const int threads = std::min(qr_threads(F8, tok), std::max(64, ((pieces + each - 1) / each + 31) / 32 * 32));
     if (tok == 1) k_qk_norm_rope<D, F8, 1><<<a.T, threads, 0, st>>>(a);
     else k_qk_norm_rope<D, F8, QR_TOKENS><<<(a.T + tok - 1) / tok, threads, 0, st>>>(a);
 }

@@ -54,6 +54,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ float silu_f32(float g) { return g / (1.0f + __expf(-g)); }
 
+// two fp32 at once
+__device__ __forceinline__ float2 both(float c) { return make_float2(c, c); }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(r))
+        : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)), "l"(reinterpret_cast<uint64_t&>(z)));
+    return r;
+}
+
 // ---------------------------------------------------------------- shared memory / mbarrier
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -161,7 +161,10 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* x) {
 }
 
 #define QR_UNROLL 3       // 32-byte pieces a thread has in flight
-#define QR_MAX_THREADS 512
+// Threads of a CTA at most.  Two such CTAs an SM bound the registers: 64 a thread at 512; 72 at 448, which the e4m3
+// chunk kernel needs, and with which four of its usual CTAs of 224 threads fit (76, and three: 27.2 us for 8,192
+// tokens instead of 23.6).
+constexpr __host__ __device__ int qr_threads(bool e4m3, int tok) { return e4m3 && tok > 1 ? 448 : 512; }
 #define QR_TOKENS 4       // tokens of a CTA on chunks
 
 // One CTA per TOK tokens.  A head is D / 16 lanes of two 16-byte chunks, so a head
@@ -177,7 +180,7 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float* x) {
 // tokens a CTA; 44 us with one token a CTA and partners 8 elements at a time by
 // shuffle (shared memory and shuffles at 80% of their rate).
 template <int D, bool E4M3, int TOK>
-__global__ void __launch_bounds__(QR_MAX_THREADS) k_qk_norm_rope(RopeArgs a) {
+__global__ void __launch_bounds__(qr_threads(E4M3, TOK), 2) k_qk_norm_rope(RopeArgs a) {
     constexpr int L = D / 16;  // lanes per head
     __shared__ float4 cs[TOK][D / 4];  // cosines and sines, two pairs to an entry, [pairs of a lane / 2][lane]: no bank twice
     __shared__ int64_t s_place[TOK];   // of the token's slot in the cache, bytes; negative: nothing is written
@@ -301,9 +304,20 @@ __global__ void __launch_bounds__(QR_MAX_THREADS) k_qk_norm_rope(RopeArgs a) {
                 const int h = is_v ? head - a.Hq - a.Hk : head - a.Hq;
                 const float* sc = is_v ? a.v_scale : a.k_scale;
                 if (sc) {
-                    const float s = 1.f / __ldg(sc + h);
+                    // The correctly rounded quotient: times 1 / scale alone, ties between two codes can fall to the
+                    // other one.  q0 + (x - q0 s) r, r = 1 / s correctly rounded (Markstein), both scaled by a power
+                    // of two that keeps the products in range; q0 as it is where it saturates anyway (infinities).
+                    float s = __ldg(sc + h);
+                    const float k = fabsf(s) < 0x1p-60f ? 0x1p64f : fabsf(s) > 0x1p60f ? 0x1p-64f : 1.f;
+                    s *= k;
+                    const float r = 1.f / s;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] *= s;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float2 v = fma2(make_float2(x[e], x[e + 1]), both(k), both(0.f)), q0 = fma2(v, both(r), both(0.f)),
+                                     q = fma2(fma2(q0, both(-s), v), both(r), q0);
+                        x[e] = fabsf(q0.x) < 512.f ? q.x : q0.x;
+                        x[e + 1] = fabsf(q0.y) < 512.f ? q.y : q0.y;
+                    }
                 }
                 uint8_t* p = (is_v ? a.v_cache : a.k_cache) + place + h * a.head_b;
                 *reinterpret_cast<uint2*>(p + d0) = pack_e4m3x8(x);

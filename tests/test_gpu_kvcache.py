@@ -202,6 +202,33 @@ def test_e4m3_without_scales_saturates(cuda_ok):
     assert torch.equal(q_out.float().nan_to_num(5), row.float().nan_to_num(5))
 
 
+def test_e4m3_writes_divide_by_the_scale(cuda_ok):
+    """x / scale, rounded once to fp32 and once to e4m3: quotients that are
+    exact ties between two codes, and scales whose reciprocal is not finite."""
+    import torch
+    scales = np.array([3.0, 7.0, 13.0, 15.0, 1e-39, 3.4e38, 0.3, 0.07], np.float32)
+    Hk, D, T, page = len(scales), 64, 16, 16
+    x = np.zeros((T, Hk, D), np.float32)
+    rng = np.random.default_rng(58)
+    for h in range(4):  # t * scale is exact in bf16, and t (5 bits) a tie between two codes
+        x[:, h] = rng.choice(np.arange(17, 32, 2), (T, D)) * scales[h]
+    x[:, 4] = rng.choice([0.0, 1e-38, -1e-38], (T, D))
+    x[:, 5] = np.clip(rng.standard_normal((T, D)), -3, 3) * 1e38
+    x[:, 6:] = rng.standard_normal((T, 2, D)) * 5
+    x = torch.as_tensor(bf16(x)).to(torch.bfloat16).cuda()
+    k = torch.zeros((1, page, Hk, D), dtype=torch.float8_e4m3fn, device="cuda")
+    v = torch.zeros_like(k)
+    sc = torch.as_tensor(scales).cuda()
+    desc = M.moe_kv_desc(k, v, Hk, sc, sc)
+    at = torch.arange(T, dtype=torch.int32, device="cuda")
+    M.moe_qk_norm_rope(desc, x, x, x, at, at, torch.empty_like(x))
+    torch.cuda.synchronize()
+    want = (x.float() / sc[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).float()
+    for cache in (k, v):
+        got = cache[0].float()
+        assert torch.equal(got, want), [int((got[:, h] != want[:, h]).sum()) for h in range(Hk)]
+
+
 def test_slot_past_the_cache_is_reported(cuda_ok):
     import torch
     k = torch.full((2, 16, 1, 64), 2.0, dtype=torch.bfloat16, device="cuda")
