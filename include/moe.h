@@ -392,8 +392,9 @@ int moe_rope_inv_freq(int kind, int rot_dim, double base, double factor, double 
  *   rows q_stride, k_stride, v_stride elements apart (one fused projection
  *   buffer serves), 16-byte aligned, strides multiples of 8; position, slot
  *   [T] int32; inv_freq [rot_dim / 2] fp32 (device); q_out rows out_stride
- *   apart, q itself (same stride) for in place; rot_dim a multiple of 16 up to
- *   head_dim, 0 = no rotation.
+ *   apart, q itself (same stride) for in place; other rows that share memory with
+ *   q, k or v are refused (rows of one stride may interleave); rot_dim a multiple
+ *   of 16 up to head_dim, 0 = no rotation.
  * A row with a negative slot is padding: nothing is written for it.  A slot past
  * the cache does the same and latches MOE_ERR_SLOT.  Slots of a call are distinct
  * (of two rows with one slot, parts of either may stay).

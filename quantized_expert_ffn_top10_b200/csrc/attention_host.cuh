@@ -29,6 +29,15 @@ inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
     return p && q && n && m && a < b + m && b < a + n;
 }
 
+// Whether T rows of w elements, s apart, and T rows of v elements, r apart, share memory.  Rows of equal strides may
+// interleave (parts of one projection buffer); unequal ones may not meet at all.
+inline bool rows_overlap(const uint16_t* p, int64_t s, int64_t w, const uint16_t* q, int64_t r, int64_t v, int T) {
+    if (!overlap(p, ((size_t)(T - 1) * s + w) * 2, q, ((size_t)(T - 1) * r + v) * 2)) return false;
+    if (s != r) return true;
+    const int64_t at = ((q - p) % s + s) % s;  // where q's rows start in p's
+    return at < w || at + v > s;
+}
+
 // Four tokens a CTA once that still leaves four CTAs for every SM; below, one token a CTA for the latency.
 template <int D, bool F8>
 void launch_rope(const RopeArgs& a, cudaStream_t st) {
@@ -317,15 +326,11 @@ int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride,
     for (const void* p : {(const void*)position, (const void*)slot, (const void*)inv_freq})
         if (!aligned(p, 4)) return MOE_ERR_ARG;
     if (!aligned(q_norm, 16) || !aligned(k_norm, 16)) return MOE_ERR_ARG;
-    // in place (the same rows) is fine: a CTA reads its token's row before it writes it; rows that
-    // merely overlap are not
-    const size_t qb = ((size_t)(T - 1) * q_stride + qw) * 2, ob = ((size_t)(T - 1) * out_stride + qw) * 2;
-    if ((q_out != q || out_stride != q_stride) && overlap(q, qb, q_out, ob)) {
-        // q and q_out may still interleave inside rows of one buffer
-        const int64_t gap = q_out - q;
-        if (q_stride != out_stride || std::llabs(gap) >= q_stride || std::llabs(gap) < qw || std::llabs(gap) + qw > q_stride)
-            return MOE_ERR_ARG;
-    }
+    // in place (the same rows) is fine: a thread reads its piece of a head before it writes it.  Rows that merely
+    // overlap are not, nor queries written over keys or values, which other warps still read
+    if ((q_out != q || out_stride != q_stride) && rows_overlap(q, q_stride, qw, q_out, out_stride, qw, T)) return MOE_ERR_ARG;
+    if (rows_overlap(k, k_stride, kw, q_out, out_stride, qw, T) || rows_overlap(v, v_stride, kw, q_out, out_stride, qw, T))
+        return MOE_ERR_ARG;
     RopeArgs a{};
     a.q = q; a.k = k; a.v = v;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.out_stride = out_stride;

@@ -119,6 +119,22 @@ def test_rope_refusals(lib):
     assert r(T=0, inv=None, rot=0) == M.MOE_OK
 
 
+def test_rope_outputs_over_its_inputs_are_refused(lib):
+    """q_out over keys or values, whole or in part: of a fused buffer with as many
+    cached heads as query heads (rows of 256 + 256 + 256), and of their own buffers."""
+    d = _desc(n_heads=2)
+    fused = dict(desc=d, qs=768, k=3 * FAKE + 512, ks=768, v=3 * FAKE + 1024, vs=768)
+    r = lambda **kw: _rope(lib, **{**fused, **kw})  # noqa: E731
+    for at in (512, 1024, 512 + 16, 1024 - 16):                # the keys, the values, parts of both
+        for token in (0, 1, 4):
+            assert r(out=3 * FAKE + at + token * 2 * 768, os_=768) == M.MOE_ERR_ARG, (at, token)
+    assert r(out=3 * FAKE + 512, os_=512) == M.MOE_ERR_ARG     # at another stride
+    own = dict(desc=d, qs=256, k=5 * FAKE, ks=256, v=6 * FAKE, vs=256, os_=256)
+    for out in (5 * FAKE, 6 * FAKE, 5 * FAKE + 512, 6 * FAKE - 16):
+        assert _rope(lib, out=out, **own) == M.MOE_ERR_ARG
+    assert _rope(lib, out=5 * FAKE + 16, **{**own, "ks": 512, "os_": 512}) == M.MOE_ERR_ARG
+
+
 def _map(lib, kv=FAKE, q=2 * FAKE, Bn=4, page=16, free=3 * FAKE, n_free=10, table=4 * FAKE, width=8, T=9, kvn=5 * FAKE,
          cu=6 * FAKE, pos=7 * FAKE, slot=8 * FAKE, used=9 * FAKE):
     return lib.moe_kv_map(kv, q, Bn, page, free, n_free, table, width, T, kvn, cu, pos, slot, used, None)
