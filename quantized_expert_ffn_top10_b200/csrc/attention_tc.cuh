@@ -350,15 +350,15 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     }
                     if (!capped) load_s();
                     if (tilted) {
-                        const float2 rs2 = make_float2(rs, rs), step = make_float2(2.f * slope, 2.f * slope);
-                        const float at0 = -slope * (float)(pos - k0);
-                        float2 bias = make_float2(at0, at0 + slope);
+                        // the bias from the column every 8 of them: a running sum over all drifts by 2^-19 of the bias
+                        const float2 rs2 = both(rs), slope2 = both(slope), at0 = both(-slope * (float)(pos - k0)), step = both(2.f * slope);
+                        float2 bias;
 #pragma unroll
                         for (int c = 0; c < 128; c += 2) {
+                            bias = c % 8 ? add2(bias, step) : fma2(make_float2((float)c, (float)(c + 1)), slope2, at0);
                             const float2 x = fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), rs2, bias);
                             u[c] = __float_as_uint(x.x);
                             u[c + 1] = __float_as_uint(x.y);
-                            bias = add2(bias, step);
                         }
                     }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

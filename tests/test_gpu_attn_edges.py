@@ -146,3 +146,36 @@ def test_never_written_places_cost_nothing(cuda_ok, page, f8):
     clean = median_us()
     c.check()
     assert stale <= 1.5 * clean, (stale, clean)
+
+
+@pytest.mark.parametrize("kv", [3000, 60000])
+@pytest.mark.parametrize("slope", [0.5, 0.31, 0.0371])
+def test_a_far_key_that_outweighs_its_bias(cuda_ok, slope, kv):
+    """One key near the start, behind all rows, whose score passes its bias by 50:
+    its softmax weight is 1 and lse is the score less the bias, both large. Eight
+    roundings to fp32 (half a step, 2^-24, of the larger of the two) is what
+    scale, slope, product and sums may add."""
+    import torch
+    n, at, D = 64, 100, 128
+    c = Case([n], [kv], Hq=4, Hk=1, page=16, slopes=True, seed=57)
+    c.slopes = np.full(4, slope, np.float32)
+    c.t_slopes = torch.as_tensor(c.slopes).cuda()
+    # q = 8 everywhere, and a key element that makes q . k scale exceed the largest bias by about 50 (whole eighths: the
+    # sum of 128 equal products is exact)
+    x = float(bf16(np.round((slope * kv + 50) * D ** 0.5 / (8 * D) * 8) / 8))
+    c.t_q.fill_(8.0)
+    c.q[:] = 8.0
+    c.cache.k.zero_()
+    c.cache.k[int(c.cache.table[0, at // 16]), at % 16] = x
+    c.run("prefill", table=wide(c))
+    torch.cuda.synchronize()
+    assert M.moe_last_device_error() == 0
+    score = 8.0 * x * D * float(np.float32(c.scale))
+    pos = kv - n + np.arange(n)
+    want = score - float(np.float32(slope)) * (pos - at)
+    near = np.exp(-want) / (1 - np.exp(-slope))  # the other keys, scores of 0, next to the row at most
+    assert want.min() > 25 and near.max() < 1e-9
+    lse = c.lse.double().cpu().numpy()
+    assert np.all(np.abs(lse - want[:, None]) <= 8 * 2.0 ** -24 * score), np.abs(lse - want[:, None]).max() / score * 2 ** 24
+    v = c.values[0][at, 0]
+    assert np.all(np.abs(c.out.double().cpu().numpy() - v) <= 1.01 * (2.0 ** -8 * np.abs(v) + 1e-8))
