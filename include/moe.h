@@ -366,8 +366,16 @@ int moe_kv_map(const int32_t* kv_len, const int32_t* q_len, int B, int page_size
  *   MOE_ROPE_PARTS   by parts: with r_i = original_len f_i / 2 pi turns over
  *                    the original context and g = clamp((r_i - beta_slow) /
  *                    (beta_fast - beta_slow), 0, 1): f_i g + f_i (1 - g) /
- *                    factor; rot_scale = 0.1 ln(factor) + 1 (the published
- *                    "YaRN" method).  rot_scale = 1 for the others.
+ *                    factor; rot_scale = 0.1 ln(factor) + 1, for the other
+ *                    kinds 1 (the formulas of the "YaRN" paper).  This ramp
+ *                    is linear in the turns.  Models scaled with the method's
+ *                    published code have one that is linear in the index i,
+ *                    between the rounded indices of pairs that turn beta_fast
+ *                    and beta_slow times; in the ramp their frequencies differ
+ *                    (by up to 42% at base 1e6, 128 dimensions, factor 4,
+ *                    32K).  For them, and wherever a model's own frequencies
+ *                    are at hand, give moe_qk_norm_rope those: it takes any
+ *                    inv_freq.
  * inv_freq [rot_dim / 2], rot_scale [1] fp32 (host).  factor >= 1, base > 1.
  * Unused numbers are ignored.  Host only, no CUDA.
  */

@@ -525,7 +525,8 @@ def moe_attn_prefill(kv: KvDesc, q, cu_q, kv_len, block_table, out, ws, scale, s
 
 def moe_rope_inv_freq(rot_dim: int, base: float, kind: int = MOE_ROPE_PLAIN, factor: float = 1.0,
                       original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
-    """(numpy fp32 [rot_dim / 2] frequencies, factor on cosine and sine); include/moe.h gives the kinds."""
+    """(numpy fp32 [rot_dim / 2] frequencies, factor on cosine and sine); include/moe.h gives the kinds, and says
+    which models' scaling MOE_ROPE_PARTS is not (theirs go to moe_qk_norm_rope as they are)."""
     import numpy as np
     f = np.zeros(max(rot_dim // 2, 1), np.float32)
     s = ctypes.c_float(0.0)

@@ -192,6 +192,25 @@ def test_frequencies_by_parts(lib):
     assert M.moe_rope_inv_freq(rot, base, M.MOE_ROPE_PARTS, 1.0, L)[1] == 1.0
 
 
+@pytest.mark.parametrize("rot,base,factor,L,fast,slow", [(128, 1e6, 4.0, 32768.0, 32.0, 1.0), (64, 1e4, 16.0, 4096.0, 32.0, 1.0),
+                                                         (96, 5e5, 2.5, 8192.0, 7.0, 0.5)])
+def test_the_ramp_of_frequencies_by_parts_is_linear_in_the_turns(lib, rot, base, factor, L, fast, slow):
+    """Every frequency against the formula, so that another ramp fails (one linear in the index, as in the method's
+    published code, is off by far more than a rounding)."""
+    f, _ = M.moe_rope_inv_freq(rot, base, M.MOE_ROPE_PARTS, factor, L, fast, slow)
+    i = np.arange(rot // 2)
+    p = base ** (-2.0 * i / rot)
+    turns = L * p / (2 * math.pi)
+    keep = np.clip((turns - slow) / (fast - slow), 0, 1)
+    ref = p * keep + p / factor * (1 - keep)
+    assert np.all(np.abs(f - ref) <= 1.01 * HALF_STEP * ref)
+    at = [rot * math.log(L / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
+    lo, hi = math.floor(at[0]), math.ceil(at[1])
+    by_index = 1 - np.clip((i - lo) / (hi - lo), 0, 1)
+    other = p * by_index + p / factor * (1 - by_index)
+    assert np.max(np.abs(f / other - 1)) > 0.1
+
+
 @pytest.mark.parametrize("args", [(3, 1e4), (0, 1e4), (64, 1.0), (64, math.nan), (64, 1e4, 4), (64, 1e4, -1),
                                   (64, 1e4, 1, 0.5), (2, 1e4, 2, 2.0), (64, 1e4, 3, 2.0, 0.0), (64, 1e4, 3, 2.0, 4096.0, 1.0, 1.0)])
 def test_frequency_refusals(lib, args):
