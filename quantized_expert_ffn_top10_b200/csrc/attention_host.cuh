@@ -351,8 +351,9 @@ int moe_qk_norm_rope(const moe_kv_desc* kv, const uint16_t* q, int64_t q_stride,
 }
 
 size_t moe_attn_workspace_bytes(int T, int B, int n_heads, int n_kv_heads, int head_dim) {
-    if (T < 0 || B < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
-        return 0;
+    if (T < 0 || T > MOE_ATTN_MAX_B * MOE_DECODE_MAX_T || B < 0 || B > MOE_ATTN_MAX_B) return 0;
+    if (n_heads < 1 || n_heads > MOE_ATTN_MAX_HEADS || n_kv_heads < 1 || n_heads % n_kv_heads) return 0;
+    if (head_dim != 64 && head_dim != 128) return 0;
     return attn_ws(head_dim).total;
 }
 

@@ -95,6 +95,13 @@ def test_attention_workspace(lib):
         assert M.moe_attn_workspace_bytes(*bad) == 0
 
 
+def test_no_workspace_for_sizes_that_no_call_takes(lib):
+    most = M.MOE_ATTN_MAX_B * M.MOE_DECODE_MAX_T
+    assert M.moe_attn_workspace_bytes(most, M.MOE_ATTN_MAX_B, M.MOE_ATTN_MAX_HEADS, 1, 64) > 0
+    for bad in ((most + 1, 1, 16, 2, 128), (5, M.MOE_ATTN_MAX_B + 1, 16, 2, 128), (5, 1, M.MOE_ATTN_MAX_HEADS + 1, 1, 64)):
+        assert M.moe_attn_workspace_bytes(*bad) == 0
+
+
 def _rope(lib, desc=None, q=3 * FAKE, qs=2560, k=3 * FAKE + 4096, ks=2560, v=3 * FAKE + 4608, vs=2560, T=5, pos=4 * FAKE,
           slot=5 * FAKE, qn=None, kn=None, eps=1e-6, inv=6 * FAKE, rot=128, scale=1.0, out=7 * FAKE, os_=2048):
     d = desc if desc is not None else _desc()
