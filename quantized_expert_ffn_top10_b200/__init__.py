@@ -390,7 +390,7 @@ def _rows16(t, n, d, where, what, dev):
             and t.get_device() == dev):
         import torch
         if t.dtype is torch.bfloat16 or t.dtype in (torch.int16, torch.uint16):
-            return t.data_ptr(), st[0] if shape[0] > 1 else max(st[0], n * d)
+            return t.data_ptr(), st[0] if shape[0] > 1 else n * d  # (a single row's stride means nothing)
     _refuse(where, f"{what} is a bf16 [T, {n}, {d}] tensor with adjacent heads on the current device")
 
 
