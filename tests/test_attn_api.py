@@ -164,11 +164,10 @@ def test_map_refusals(lib):
 def test_a_single_row_may_have_any_stride():
     """One row out of a buffer whose rows are no multiple of 8 elements apart."""
     import torch
-    x = torch.zeros(3, 4 * 64 + 3, dtype=torch.bfloat16)
-    row = x[:1, :4 * 64].view(1, 4, 64)
-    assert row.stride(0) == 4 * 64 + 3
-    assert M._rows16(row, 4, 64, "here", "q", -1) == (x.data_ptr(), 4 * 64)
-    assert M._rows16(x[:2, :4 * 64].view(2, 4, 64), 4, 64, "here", "q", -1)[1] == 4 * 64 + 3  # the library refuses these
+    x = torch.zeros(3, 4 * 64 + 3, dtype=torch.bfloat16)[:, :4 * 64].unflatten(1, (4, 64))
+    assert x[:1].stride(0) == 4 * 64 + 3
+    assert M._rows16(x[:1], 4, 64, "here", "q", -1) == (x.data_ptr(), 4 * 64)
+    assert M._rows16(x[:2], 4, 64, "here", "q", -1)[1] == 4 * 64 + 3  # the library refuses these
 
 
 def test_strerror_names_the_page_error(lib):
