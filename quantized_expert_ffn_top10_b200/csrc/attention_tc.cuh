@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(qready);
-            const float rs = a.scale * ks * unit * LOG2E;
+            // (above zero where it multiplies hidden scores, -inf: queries of zeros under a scale of 2^-64 underflow it)
+            const float rs0 = a.scale * ks * unit * LOG2E, rs = simple ? fmaxf(rs0, 1.17549435e-38f) : rs0;
             const AttCap cap(a.softcap);
             float m = -INFINITY, l = 0.f;
             for (int n = 0; n < steps; ++n) {

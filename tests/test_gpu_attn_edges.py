@@ -179,3 +179,18 @@ def test_a_far_key_that_outweighs_its_bias(cuda_ok, slope, kv):
     assert np.all(np.abs(lse - want[:, None]) <= 8 * 2.0 ** -24 * score), np.abs(lse - want[:, None]).max() / score * 2 ** 24
     v = c.values[0][at, 0]
     assert np.all(np.abs(c.out.double().cpu().numpy() - v) <= 1.01 * (2.0 ** -8 * np.abs(v) + 1e-8))
+
+
+@pytest.mark.parametrize("tables", ["tight", "wide"])
+@pytest.mark.parametrize("scale", [2.0 ** -64, 1e-30, 0.1])
+def test_queries_of_zeros_and_tiny_ones_with_an_e4m3_cache(cuda_ok, scale, tables):
+    """Their scores are zero, or as good as: the mean of the values that they see."""
+    import torch
+    c = Case([50, 9], [390, 4], Hq=4, Hk=2, page=16, f8=True, seed=86)
+    gain = np.resize(2.0 ** np.array([0, -90, -120, 0, -20]), 59)
+    c.q = bf16(c.q * gain[:, None, None])
+    c.q[0::5] = 0.0
+    c.t_q = torch.as_tensor(c.q).to(torch.bfloat16).cuda()
+    c.scale = scale
+    c.run("prefill", table=wide(c) if tables == "wide" else None)
+    c.check()
