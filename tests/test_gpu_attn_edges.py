@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import quantized_expert_ffn_top10_b200 as M
+from attn_power import marked_limits, marked_rows, marks, noise_rows
 from attn_ref import attn_limits, bf16
 from test_gpu_attn import Case
 
@@ -179,6 +180,62 @@ def test_a_far_key_that_outweighs_its_bias(cuda_ok, slope, kv):
     assert np.all(np.abs(lse - want[:, None]) <= 8 * 2.0 ** -24 * score), np.abs(lse - want[:, None]).max() / score * 2 ** 24
     v = c.values[0][at, 0]
     assert np.all(np.abs(c.out.double().cpu().numpy() - v) <= 1.01 * (2.0 ** -8 * np.abs(v) + 1e-8))
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("which,q_len,kv_len,Hq,Hk,page,window,tables", [
+    ("decode", [1], [131072], 8, 1, 64, 0, "tight"), ("decode", [5], [131072], 16, 2, 64, 0, "tight"),
+    ("decode", [2] * 5, [40000, 129, 77777, 1, 30011], 8, 1, 16, 0, "tight"),
+    ("decode", [5, 1, 3], [60000, 20001, 128], 16, 2, 256, 0, "wide"), ("decode", [4], [70001], 8, 1, 16, 33333, "tight"),
+    ("prefill", [300, 7], [20000, 33333], 4, 2, 16, 0, "wide"), ("prefill", [129], [40003], 4, 1, 24, 0, "wide"),
+    ("prefill", [513, 40], [30000, 9000], 8, 1, 64, 5000, "wide"), ("prefill", [20, 3], [3000, 1111], 4, 1, 16, 0, "tight")])
+def test_every_key_counts_once(cuda_ok, which, q_len, kv_len, Hq, Hk, page, window, tables, f8):
+    """Equal scores (queries of zeros), and one value element per run of 128
+    keys that is 1: every sum is a whole number, so the output is a count over
+    the number of visible keys, and a run left out or added twice moves it."""
+    import torch
+    D = 128
+    c = Case(q_len, kv_len, Hq=Hq, Hk=Hk, D=D, page=page, f8=f8, scales=False, window=window, seed=59)
+    c.t_q.zero_()
+    c.cache.v.zero_()
+    for b, n in enumerate(kv_len):
+        j = torch.arange(n, device="cuda")
+        rows = c.cache.table_dev[b, (j // page).long()].long()
+        at = torch.as_tensor(marks(n, D)).cuda()
+        if f8:
+            c.cache.v.view(torch.uint8)[rows, j % page, :, at] = 0x38  # 1.0
+        else:
+            c.cache.v[rows, j % page, :, at] = 1.0
+    c.run(which, table=wide(c, 1 << 18) if tables == "wide" else None)
+    torch.cuda.synchronize()
+    assert M.moe_last_device_error() == 0
+    out, want = marked_rows(q_len, kv_len, window, D)
+    lim, lse_lim = marked_limits(out, want)
+    got, lse = c.out.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    bad = ~(np.abs(got - out[:, None]) <= lim[:, None])
+    assert not bad.any(), np.argwhere(bad)[0]
+    empty = np.isneginf(want)
+    assert np.isneginf(lse[empty]).all()
+    assert np.all(np.abs(lse[~empty] - want[~empty][:, None]) <= lse_lim[~empty][:, None])
+
+
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("which,n,kv,Hq,Hk,page", [("decode", 5, 131072, 4, 2, 64), ("decode", 5, 131072, 16, 2, 64),
+                                                   ("prefill", 40, 50000, 4, 2, 16)])
+def test_long_caches_in_norm(cuda_ok, which, n, kv, Hq, Hk, page, f8):
+    """Random keys and values: a bound of each row's error in the 2-norm, tight
+    enough that one run of 128 keys left out breaks it (test_attn_power.py)."""
+    import torch
+    c = Case([n], [kv], Hq=Hq, Hk=Hk, page=page, f8=f8, seed=60)
+    c.run(which)
+    torch.cuda.synchronize()
+    assert M.moe_last_device_error() == 0
+    got = c.out.double().cpu().numpy()
+    for h in range(0, Hq, Hq // 4):
+        K, V = (x[0][:, h // (Hq // Hk)].astype(np.float64) for x in (c.keys, c.values))
+        out, bound = noise_rows(c.q[:, h], K, V, c.scale, f8)
+        off = np.linalg.norm(got[:, h] - out, axis=1)
+        assert np.all(off <= bound), (h, (off / bound).max())
 
 
 @pytest.mark.parametrize("tables", ["tight", "wide"])
