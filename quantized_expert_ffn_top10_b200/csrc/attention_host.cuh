@@ -198,11 +198,11 @@ cudaError_t launch_attn_chunk(AttnArgs a, int sms, cudaStream_t st) {
 // Which kernel.  `rows`: the most rows of one request that share a cached head.  Up to 16 the row
 // kernels read the cache at memory speed and waste no tensor work on absent rows (64 requests of 8 rows
 // at 32K: 185 us, the chunk kernel 383; of 16 rows at 16K: 242 us, 278).  Above, the chunk kernel does
-// (48 windows of 24 rows at 20K: 144 us, row kernel 196; 64 of 40 rows at 16K: 305 us, 520), except
-// that it takes longer to start and end, so a small call (query rows x keys the table can hold below
-// 2^19) stays with the row kernels (5 tokens of 8 heads a cached one at 1,000 keys: 15.4 us, the chunk
-// kernel 22; 37 tokens at 8,192: 39 us, 34), and that capped scores cost it more (24 windows of 25 rows
-// in a 4K sliding window: 89 us, 110).
+// (48 windows of 24 rows at 20K: 144 us, row kernel 196, capped at 30: 316 us, 445; 64 of 40 rows at 16K:
+// 305 us, 520), except that it takes longer to start and end, so a small call (query rows x keys the table
+// can hold below 2^19) stays with the row kernels (5 tokens of 8 heads a cached one at 1,000 keys: 15.4 us,
+// the chunk kernel 22; 37 tokens at 8,192: 39 us, 34).  The bound is on what the table can hold because
+// only the device knows the lengths.
 template <int D, bool F8>
 cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     const int64_t rows = (int64_t)std::min(a.max_q, a.T) * a.G;
@@ -210,7 +210,7 @@ cudaError_t launch_attn(const AttnArgs& a, int sms, cudaStream_t st) {
     if (rows <= 16) return launch_attn_rows<D, F8, 2, 1, 4>(a, sms, st);
     const int64_t keys = std::min((int64_t)a.width * a.page_size, (int64_t)MOE_ATTN_MAX_KV);
     const bool small = (int64_t)a.T * a.G * keys < 1 << 19;
-    if (rows <= 32 && (small || a.softcap > 0.f)) return launch_attn_rows<D, F8, 2, 2, 2>(a, sms, st);
+    if (rows <= 32 && small) return launch_attn_rows<D, F8, 2, 2, 2>(a, sms, st);
     return small ? launch_attn_rows<D, F8, 2, 4, 2>(a, sms, st) : launch_attn_chunk<D, F8>(a, sms, st);
 }
 
