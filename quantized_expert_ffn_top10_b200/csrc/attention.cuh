@@ -633,8 +633,9 @@ __global__ void __launch_bounds__(AttCfg<D, F8, NTW, RW, KW>::NTH, AttCfg<D, F8,
                         p[e] = ex2(s[nt][u][e] - ref[e & 1]);
                         l[nt][e & 1] += p[e];
                     }
-                    // the numerators are rounded once more, to the cache's 16-bit type, for the product with V;
-                    // the sum above takes them unrounded
+                    // the numerators are rounded once more for the product with V, to bf16 (2^-8) or, beside e4m3
+                    // values, fp16 (2^-11): an MMA takes one type, and fp32 values would need the tf32 form at half
+                    // its rate and twice the registers; the sum above takes them unrounded
                     pb[nt][u][0] = mat_t(F8 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]));
                     pb[nt][u][1] = mat_t(F8 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]));
                 }

@@ -15,9 +15,9 @@
 // was taken: numerators stay below 2^8 (2^14 in fp16), which costs no precision,
 // and after the first tiles it hardly ever happens.
 //
-// Roles (16 warps, registers moved from the lower eight roles' warps to the softmax's): 0-3 and 4-7 the softmax of the two halves, 12 the MMAs, 13 the
-// TMA loads (a box per page and 64 columns), 8-11 what the loads need beside
-// that: e4m3 rows widened to fp16 (exactly; the queries are then scaled per row by
+// Roles (16 warps; warps 8 to 15 give registers up to the softmax): 0-3 and 4-7 the
+// softmax of the two halves, 12 the MMAs, 13 the TMA loads (a box per page and 64
+// columns), 8-11 what the loads need beside that: e4m3 rows widened to fp16 (exactly; the queries are then scaled per row by
 // a power of two, as in the row kernel), non-finite values of partly masked V
 // tiles set aside, and the whole gather, row by row, for page sizes that TMA boxes
 // do not tile (not a power of two, or below 8).
@@ -289,7 +289,10 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                     tc_fence_after();
                     const int k0 = cur.lo + (cur.tile + j) * AC_TK;
                     const bool masked = __any_sync(~0u, k0 < lo || k0 > hi - AC_TK), edit = masked || !simple;
-                    const bool tilted = MODE == 1 && !masked && !__any_sync(~0u, mine && k0 + AC_TK - 1 > pos);
+                    // (two forms of the same: 2,048 tokens with slopes at 64K take 1.39 ms in the first for e4m3, 1.47 in
+                    // the second; for bf16 1.39 and 1.30)
+                    const bool tilted = MODE == 1 && !masked && (F8 ? __all_sync(~0u, !mine || k0 + AC_TK - 1 <= pos)
+                                                                    : !__any_sync(~0u, mine && k0 + AC_TK - 1 > pos));
                     // Scores that are not S times a number, or hidden ones, are put in S's place first; but a slope
                     // alone is linear in the column of a tile behind the row, and is added to the registers below.
                     uint32_t u[128];
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                             }
                         }
                     }
-                    if (edit && !tilted && !capped) {
+                    if (F8 && MODE == 1 ? !tilted : edit && !tilted && !capped) {
                         const int f = masked ? lo - k0 : -1024, e = masked ? hi - k0 : 1024;  // visible columns [f, e)
                         const float p0 = (float)(pos - k0);
 #pragma unroll 1
@@ -387,7 +390,9 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m - LIFT;
-                    // numerators, their sum unrounded, and their 16-bit form over S
+                    // Numerators, their sum unrounded, and their 16-bit form over S: bf16 (2^-8) beside bf16 values, since
+                    // an MMA takes one type and fp16 lacks bf16's range; fp16 (2^-11) beside e4m3 ones, which it holds
+                    // exactly.  A second 16-bit part would be half as many products again.
                     const float2 mul2 = make_float2(mul, mul), ref2 = make_float2(-ref, -ref);
                     float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
@@ -747,7 +752,7 @@ __global__ void __launch_bounds__(AC_THREADS, 1)
                         if (duo || h == 0) ok = mbar_wait_fast(full + ks, k_ph, 25, ks);
                         if (!ok) break;
                         tc_fence_after();
-                        // (addresses count in 16 bytes; rolled loops, or the descriptors are kept in registers)
+                        // (descriptor addresses count in 16 bytes)
                         uint64_t da = make_sdesc_sw128(sq + h * TILE), db = make_sdesc_sw128(ring + ks * TILE);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
